@@ -43,12 +43,20 @@ class MoeLayer(ctypes.Structure):
                 ("routed", MoeBank), ("shared", MoeBank)]
 
 
+class MoeMatrix(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("x_type", ctypes.c_int32), ("y_type", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("s", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 _LIB = None
 EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_size",
            "moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_forward_marked", "moe_device_status", "moe_launches_per_call",
            "moe_layer_forward_static", "moe_static_device_status", "moe_test_inject_hold",
-           "moe_nvfp4_pack_scales", "moe_nvfp4_quantize_rows", "moe_device_wait_site"]
+           "moe_nvfp4_pack_scales", "moe_nvfp4_quantize_rows", "moe_device_wait_site",
+           "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec"]
 
 
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
@@ -65,6 +73,7 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     LP = ctypes.POINTER(MoeLayer)
+    MP = ctypes.POINTER(MoeMatrix)
     sig = {
         "moe_abi_version": (I32, []),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -85,6 +94,9 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "moe_test_inject_hold": (I32, [LP, P, SZ, I32, I32, P]),
         "moe_nvfp4_pack_scales": (I32, [P, P, I32, I32, I32, P]),
         "moe_nvfp4_quantize_rows": (I32, [P, I32, I32, P, P, P, P]),
+        "moe_matvec_validate": (I32, [MP]),
+        "moe_matvec_workspace_size": (SZ, [MP]),
+        "moe_matvec": (I32, [MP, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -334,3 +346,122 @@ def test_inject_hold(L: MoeLayer, ws, hold: bool, budget_cycles: int = 0, stream
     _check(load_library().moe_test_inject_hold(ctypes.byref(L), ws.data_ptr(), ws.numel(),
                                                int(bool(hold)), int(budget_cycles),
                                                _stream(stream)), "moe_test_inject_hold")
+
+
+# ---------------------------------------------------------------------- dense operators
+#
+# Unlike the layer's calls above, these check their tensors (type, shape, layout, device)
+# before handing over pointers, and raise ValueError. The work runs on the tensors' device,
+# on its current stream unless one is given.
+
+
+def _dtype_code(t) -> int:
+    import torch
+    try:
+        return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[t]
+    except KeyError:
+        raise ValueError(f"element type {t} is not supported") from None
+
+
+def _check_rows(t, name, rows, cols, dtype, device):
+    """A [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected {dtype} [{rows}, {cols}] on {device}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+
+
+def _check_ws(ws, device):
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {device}")
+
+
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current; returns its status."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _alloc_zeroed(nbytes: int, device):
+    """A zeroed workspace whose fill is waited for (see alloc_workspace)."""
+    import torch
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
+class QuantMatrix:
+    """A weight matrix [N, K] of 4-bit integers with group scales, on the device: ``codes``
+    int32 [N, K/8] (8 two's-complement nibbles a word along K), ``scales`` bf16
+    [N, K/group], ``bias`` fp32 [N] or None (the int4 encoding of the expert banks)."""
+
+    def __init__(self, codes, scales, K: int, group: int = 128, bias=None):
+        import torch
+        if group not in (32, 64, 128) or K < 1 or K % group:
+            raise ValueError(f"K must be a multiple of the group (32, 64 or 128): {K}, {group}")
+        if codes.dim() != 2 or not codes.is_cuda:
+            raise ValueError("codes must be a CUDA tensor [N, K/8]")
+        N, dev = codes.shape[0], codes.device
+        if codes.dtype not in (torch.int32, torch.uint32):
+            raise ValueError("codes must hold 32-bit words")
+        _check_rows(codes, "codes", N, K // 8, codes.dtype, dev)
+        _check_rows(scales, "scales", N, K // group, torch.bfloat16, dev)
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or
+                                 bias.device != dev or not bias.is_contiguous()):
+            raise ValueError(f"bias: expected contiguous fp32 [{N}] on {dev}")
+        self.codes, self.scales, self.bias = codes, scales, bias
+        self.N, self.K, self.group, self.device = N, K, group, dev
+
+    def descriptor(self, T: int, x_dtype=None, y_dtype=None, ldx: int | None = None,
+                   ldy: int | None = None) -> MoeMatrix:
+        """The call's descriptor: T rows of x_dtype (bf16 by default) giving rows of y_dtype
+        (x_dtype by default, or fp32); ldx, ldy: elements between rows (dense by default).
+        It holds pointers into this object's tensors, which must outlive it."""
+        import torch
+        x_dtype = torch.bfloat16 if x_dtype is None else x_dtype
+        y_dtype = x_dtype if y_dtype is None else y_dtype
+        M = MoeMatrix(T, self.N, self.K, self.group, _dtype_code(x_dtype), _dtype_code(y_dtype),
+                      self.K if ldx is None else ldx, self.N if ldy is None else ldy,
+                      self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.bias))
+        M.owner = self
+        M.dtypes = (x_dtype, y_dtype)
+        _check(load_library().moe_matvec_validate(ctypes.byref(M)), "moe_matvec_validate")
+        return M
+
+
+def matvec_workspace_size(M: MoeMatrix) -> int:
+    return load_library().moe_matvec_workspace_size(ctypes.byref(M))
+
+
+def alloc_matvec_workspace(M: MoeMatrix):
+    return _alloc_zeroed(matvec_workspace_size(M), M.owner.device)
+
+
+def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
+    """y = x W^T (+ bias) for the T <= 32 rows of x: [T, K] -> [T, N] (include/moe_b200.h)."""
+    import torch
+    dev, (xt, yt) = M.owner.device, M.dtypes
+    _check_rows(x, "x", M.T, M.K, xt, dev)
+    if M.T > 1 and x.stride(0) != M.ldx:
+        raise ValueError(f"x: rows are {x.stride(0)} elements apart, the descriptor says {M.ldx}")
+    if out is None:
+        out = torch.empty((M.T, M.ldy), dtype=yt, device=dev)
+        if M.ldy != M.N:
+            out = out[:, :M.N]
+    else:
+        _check_rows(out, "out", M.T, M.N, yt, dev)
+        if M.T > 1 and out.stride(0) != M.ldy:
+            raise ValueError(f"out: rows are {out.stride(0)} elements apart, the descriptor says "
+                             f"{M.ldy}")
+    _check_ws(ws, dev)
+    _check(_call(dev, stream, load_library().moe_matvec, ctypes.byref(M), x.data_ptr(),
+                 out.data_ptr(), ws.data_ptr(), ws.numel()), "moe_matvec")
+    return out

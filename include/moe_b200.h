@@ -90,6 +90,13 @@ typedef enum {
 
 typedef enum { MOE_W_BF16 = 16, MOE_W_INT8 = 8, MOE_W_INT4 = 4, MOE_W_NVFP4 = 41 } moe_wfmt;
 
+/* Element types of the dense operators' activations and results. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
+
+/* Activations of the dense gated block: silu(g) = g / (1 + e^-g), and gelu in its tanh form
+ * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 } moe_act;
+
 /* Which kernels run. AUTO picks the single-kernel layer (FUSED) for 1-token calls with
  * int4 banks when the device fits it, the split-K GEMV kernels for other calls of 1..32
  * rows, and the tensor-core (tcgen05) grouped GEMMs from 33 rows up. Up to 32 rows, AUTO is
@@ -284,6 +291,43 @@ MOE_API moe_status moe_nvfp4_pack_scales(const void* src, void* dst, int32_t n_m
  * every pointer 16-byte aligned (g: 4). Enqueued on `stream`. */
 MOE_API moe_status moe_nvfp4_quantize_rows(const float* v, int32_t rows, int32_t K, void* codes,
                                            void* scales, float* g, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ dense operators
+ *
+ * Operators of the dense parts that stand beside the routed layer. They follow the
+ * conventions above (device pointers, caller-owned memory, host-side validation, a status
+ * from every call) with descriptors of their own. */
+
+/* One matrix of 4-bit integers with group scales times up to 32 rows:
+ *   y[t][n] = sum_k q[n][k] * s[n][k / group] * x[t][k] (+ bias[n])
+ * in the MOE_W_INT4 encoding (codes uint32 [N][K / 8], scales bf16 [N][K / group]). Each
+ * group's products are summed in fp32 with the codes exact, the group sums in fp32 times
+ * their scale, and the result is rounded once to y_type.
+ * 1 <= T <= 32, N >= 1, group 32, 64 or 128, K % group == 0, 1 <= K <= 32768, N <= 2^24. x_type
+ * MOE_T_BF16 or MOE_T_FP16; y_type x_type or MOE_T_FP32. ldx, ldy: elements between rows
+ * (ldx >= K and a multiple of 8, ldy >= N). w and x 16-byte aligned, s 2, y 4 for fp32 and
+ * else 2, bias (fp32 [N] or NULL) 4. y must not overlap an input. */
+typedef struct {
+  int32_t T, N, K, group;
+  int32_t x_type, y_type; /* moe_dtype */
+  int64_t ldx, ldy;
+  const void* w;
+  const void* s;
+  const float* bias;
+} moe_matrix;
+
+/* Host-side validation of a matrix descriptor (no CUDA call is made). */
+MOE_API moe_status moe_matvec_validate(const moe_matrix* M);
+
+/* Bytes of device workspace of a call (0 if M is invalid; at least 256): as for the layer,
+ * caller-owned, 256-byte aligned, zeroed once before its first use, reusable by calls ordered on
+ * one stream and not shared by calls that can overlap (two captured graphs that replay at
+ * once need one each). */
+MOE_API size_t moe_matvec_workspace_size(const moe_matrix* M);
+
+/* y = x W^T (+ bias), one kernel. x [T][ldx], y [T][ldy]. */
+MOE_API moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,185 @@
+"""The 4-bit matrix-vector product on the GPU against a plain implementation in 64 bits."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from dense_helpers import assert_close, dequantise, matvec_additions, matvec_ref, pack, quantise
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def B():
+    from expert_routed_ffn_route_b200 import binding
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    binding.load_library()
+    return binding
+
+
+def make(B, T, N, K, group, x_dtype=BF, y_dtype=None, bias=False, seed=0, **kw):
+    gen = torch.Generator().manual_seed(seed)
+    codes, scales = quantise(gen, N, K, group)
+    b = torch.randn(N, generator=gen) if bias else None
+    x = torch.randn(T, K, generator=gen).to(x_dtype)
+    m = B.QuantMatrix(codes.cuda(), scales.cuda(), K, group, bias=None if b is None else b.cuda())
+    desc = m.descriptor(T, x_dtype=x_dtype, y_dtype=y_dtype, **kw)
+    return desc, x, dequantise(codes, scales, group), b
+
+
+def check(y, x, W, b, group, what=""):
+    ref, mag = matvec_ref(x, W, b)
+    bound = mag * matvec_additions(W.shape[1], group) * 2.0 ** -23
+    return assert_close(y, ref, bound, y.dtype, what)
+
+
+SHAPES = [
+    # T, N, K, group: one output, one group; ragged rows; K that ends inside a slot; K parts
+    (1, 1, 32, 32), (1, 1, 128, 128), (1, 17, 64, 64), (2, 15, 96, 32), (3, 16, 192, 64),
+    (1, 1000, 2560, 128), (5, 130, 1312, 32), (7, 333, 4160, 64), (8, 2560, 1024, 128),
+    (9, 77, 640, 128), (16, 300, 1056, 32), (17, 33, 2560, 128), (32, 1000, 2560, 128),
+    (32, 129, 10240, 32), (31, 65, 32768, 64), (1, 40, 32768, 128), (24, 2500, 768, 128),
+    (1, 40000, 256, 128), (4, 20000, 384, 64),
+]
+
+
+@pytest.mark.parametrize("T,N,K,group", SHAPES)
+@pytest.mark.parametrize("x_dtype,y_dtype", [(BF, BF), (HF, F32), (BF, F32), (HF, HF)])
+def test_matches_64_bits(B, T, N, K, group, x_dtype, y_dtype):
+    desc, x, W, b = make(B, T, N, K, group, x_dtype, y_dtype, bias=(N % 2 == 1), seed=N + K)
+    ws = B.alloc_matvec_workspace(desc)
+    xd = x.cuda()
+    y = B.matvec(desc, xd, ws)
+    y2 = B.matvec(desc, xd, ws)  # the same workspace again: its counters are back at zero
+    assert y.dtype == y_dtype and tuple(y.shape) == (T, N)
+    assert torch.equal(y, y2)
+    check(y, x, W, b, group, f"{T}x{N}x{K} g{group}")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x_dtype", [BF, HF])
+def test_every_code_and_position_is_exact(B, group, x_dtype):
+    """One-hot rows pick single weights out: the result is that code times its scale, exactly
+    (products of 4 and 8 significant bits), wherever in the row it stands."""
+    K, N = 2 * group + 128 if group != 32 else 416, 16
+    q = torch.arange(N * K).view(N, K) * 7 % 16 - 8
+    scales = torch.tensor([2.0 ** (i % 5 - 2) for i in range(N * (K // group))]).view(N, -1).to(BF)
+    m = B.QuantMatrix(pack(q).cuda(), scales.cuda(), K, group)
+    W = dequantise(pack(q), scales, group)
+    assert torch.equal(W, q.double() * scales.double().repeat_interleave(group, 1))
+    for k0 in range(0, K, 32):
+        x = torch.zeros(32, K, dtype=x_dtype)
+        x[torch.arange(32), k0 + torch.arange(32)] = 1.5
+        desc = m.descriptor(32, x_dtype=x_dtype, y_dtype=F32)
+        y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+        assert torch.equal(y.cpu().double(), 1.5 * W[:, k0:k0 + 32].T), k0
+
+
+def test_strided_rows_and_what_lies_between_them(B):
+    T, N, K = 6, 50, 256
+    desc, x, W, b = make(B, T, N, K, 128, ldx=K + 24, ldy=N + 13, bias=True)
+    xb = torch.full((T, K + 24), float("nan"), dtype=BF, device="cuda")
+    xb[:, :K] = x.cuda()
+    yb = torch.full((T + 1, N + 13), 7.0, dtype=BF, device="cuda")
+    B.matvec(desc, xb[:, :K], B.alloc_matvec_workspace(desc), out=yb[:T, :N])
+    check(yb[:T, :N], x, W, b, 128)
+    assert (yb[:, N:] == 7).all() and (yb[T:] == 7).all()
+    # the output made by the call has the descriptor's row distance
+    y = B.matvec(desc, xb[:, :K], B.alloc_matvec_workspace(desc))
+    assert y.stride(0) == N + 13 and torch.equal(y, yb[:T, :N])
+
+
+@pytest.mark.parametrize("T", [1, 9, 32])
+def test_infinities_and_nan_stay_in_their_rows(B, T):
+    """An infinite or NaN activation reaches its own row only, with the signs of the codes."""
+    N, K = 64, 512
+    desc, x, W, b = make(B, T, N, K, 128, y_dtype=F32)
+    x[T - 1, 300] = float("inf")
+    ws = B.alloc_matvec_workspace(desc)
+    y = B.matvec(desc, x.cuda(), ws).cpu()
+    expect = torch.where(W[:, 300] == 0, torch.tensor(float("nan"), dtype=torch.float64),
+                         torch.sign(W[:, 300]) * float("inf"))
+    assert torch.equal(torch.isnan(y[T - 1]), torch.isnan(expect))
+    ok = ~torch.isnan(expect)
+    assert torch.equal(y[T - 1].double()[ok], expect[ok])
+    x[T - 1, 300] = float("nan")
+    y = B.matvec(desc, x.cuda(), ws).cpu()
+    assert torch.isnan(y[T - 1]).all()
+    if T > 1:
+        check(y[:T - 1], x[:T - 1], W, b, 128)
+
+
+def test_large_activations_overflow_only_where_the_result_does(B):
+    """Codes enter the products without an offset: activations near the end of bf16's range
+    do not overflow where codes of both signs cancel."""
+    K, N = 256, 16
+    q = torch.ones(N, K, dtype=torch.int64)
+    q[:, 1::2] = -1
+    m = B.QuantMatrix(pack(q).cuda(), torch.ones(N, K // 128, dtype=BF).cuda(), K, 128)
+    desc = m.descriptor(1, y_dtype=F32)
+    x = torch.full((1, K), 2.0 ** 120, dtype=BF)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+    assert (y == 0).all()
+
+
+@pytest.mark.parametrize("T,K", [(1, 2560), (32, 10240)])
+def test_captured_replayed_and_on_another_stream(B, T, K):
+    """Two captured graphs with a workspace each, replayed at once on two streams."""
+    N = 777
+    calls = []
+    for seed in (1, 2):
+        desc, x, W, b = make(B, T, N, K, 128, seed=seed)
+        calls.append(dict(desc=desc, x=x.cuda(), xc=x, W=W, ws=B.alloc_matvec_workspace(desc),
+                          y=torch.empty(T, N, dtype=BF, device="cuda"), g=torch.cuda.CUDAGraph(),
+                          s=torch.cuda.Stream()))
+        B.matvec(desc, calls[-1]["x"], calls[-1]["ws"], out=calls[-1]["y"])
+    torch.cuda.synchronize()
+    for c in calls:
+        with torch.cuda.graph(c["g"], stream=c["s"]):
+            B.matvec(c["desc"], c["x"], c["ws"], out=c["y"])
+        c["y"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c in calls:
+            with torch.cuda.stream(c["s"]):
+                c["g"].replay()
+    torch.cuda.synchronize()
+    for c in calls:
+        check(c["y"], c["xc"], c["W"], None, 128)
+        s = torch.cuda.Stream()
+        y = B.matvec(c["desc"], c["x"], c["ws"], stream=s)
+        s.synchronize()
+        assert torch.equal(y, c["y"])
+
+
+def test_a_row_comes_out_the_same_whatever_the_others_hold(B):
+    T, N, K = 8, 96, 1280
+    desc, x, W, b = make(B, T, N, K, 128)
+    ws = B.alloc_matvec_workspace(desc)
+    y = B.matvec(desc, x.cuda(), ws)
+    x2 = torch.randn(T, K).to(BF)
+    x2[3] = x[5]
+    y2 = B.matvec(desc, x2.cuda(), ws)
+    assert torch.equal(y2[3], y[5])
+
+
+def test_same_encoding_as_an_expert_bank(B):
+    """A projection of an int4 expert bank, taken as one matrix, equals the bank's own
+    dequantised product."""
+    from expert_routed_ffn_route_b200 import synth
+    from oracle import moe_oracle as O
+    cfg = synth.LayerConfig("mv", T=3, d=256, E=4, k=2, f=128, fmt="int4", seed=5)
+    L = synth.make_layer(cfg)
+    dl = B.DeviceLayer(L)
+    bank = dl.banks["routed"]
+    m = B.QuantMatrix(bank["w_down"][2], bank["s_down"][2], cfg.f)
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(3, cfg.f, generator=gen).to(BF)
+    desc = m.descriptor(3, y_dtype=F32)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+    arrays = L.routed.arrays()
+    W = dequantise(torch.from_numpy(arrays["w_down"][2].view("int32")),
+                   torch.from_numpy(arrays["s_down"][2].view("int16")).view(BF), 128)
+    assert W.shape == (cfg.d, cfg.f) and O is not None
+    check(y, x, W, None, 128)
