@@ -13,7 +13,8 @@ import numpy as np
 
 from . import _build
 
-FMT_CODE = {"bf16": 16, "int8": 8, "int4": 4, "nvfp4": 41}
+FMT_CODE = {"bf16": 16, "int8": 8, "int4": 4, "nvfp4": 41, "fp16": 17}
+ACT_CODE = {"silu": 0, "gelu": 1}
 PATH_CODE = {"auto": 0, "gemv": 1, "tc": 2, "fused": 3}
 N_MARKS = 6
 
@@ -50,13 +51,19 @@ class MoeMatrix(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("s", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class MoeFfn(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("f", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("bank", MoeBank)]
+
+
 _LIB = None
 EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_size",
            "moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward",
            "moe_layer_forward_marked", "moe_device_status", "moe_launches_per_call",
            "moe_layer_forward_static", "moe_static_device_status", "moe_test_inject_hold",
            "moe_nvfp4_pack_scales", "moe_nvfp4_quantize_rows", "moe_device_wait_site",
-           "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec"]
+           "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec", "moe_ffn_validate",
+           "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_device_status"]
 
 
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
@@ -74,6 +81,7 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     LP = ctypes.POINTER(MoeLayer)
     MP = ctypes.POINTER(MoeMatrix)
+    FP = ctypes.POINTER(MoeFfn)
     sig = {
         "moe_abi_version": (I32, []),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -97,6 +105,11 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "moe_matvec_validate": (I32, [MP]),
         "moe_matvec_workspace_size": (SZ, [MP]),
         "moe_matvec": (I32, [MP, P, P, P, SZ, P]),
+        "moe_ffn_validate": (I32, [FP]),
+        "moe_ffn_workspace_size": (SZ, [FP, I32]),
+        "moe_ffn_forward": (I32, [FP, P, P, P, P, SZ, P]),
+        "moe_ffn_backward": (I32, [FP, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_ffn_device_status": (I32, [FP, P, SZ, ctypes.POINTER(I32), ctypes.POINTER(I32), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -465,3 +478,134 @@ def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     _check(_call(dev, stream, load_library().moe_matvec, ctypes.byref(M), x.data_ptr(),
                  out.data_ptr(), ws.data_ptr(), ws.numel()), "moe_matvec")
     return out
+
+
+class DeviceFfn:
+    """A dense gated feed-forward block y = Wd (act(Wg x) * (Wu x)) on the device. ``bank``: a
+    bank dict as for the layer, of one expert: fmt "bf16", "fp16" or "int4" (group 128, s_*
+    scales), device tensors w_gate, w_up [f, d] and w_down [d, f] (a leading dimension of 1 is
+    accepted; int4: int32 words, K/8 a row). act: "silu" or "gelu" (tanh form)."""
+
+    def __init__(self, bank: dict, d: int, f: int, act: str = "silu"):
+        import torch
+        if act not in ACT_CODE:
+            raise ValueError(f"act must be one of {sorted(ACT_CODE)}")
+        if bank.get("n_exp", 1) != 1 or bank["fmt"] not in ("bf16", "fp16", "int4"):
+            raise ValueError("the block takes a bank of one expert in bf16, fp16 or int4")
+        fmt = bank["fmt"]
+        if fmt == "int4" and bank.get("group", 128) != 128:
+            raise ValueError("int4 blocks have groups of 128")
+        step = 128 if fmt == "int4" else 8
+        if d < step or f < step or d % step or f % step:
+            raise ValueError(f"d and f must be multiples of {step}: {d}, {f}")
+        self.dtype = torch.float16 if fmt == "fp16" else torch.bfloat16
+        self.device = bank["w_gate"].device
+        if self.device.type != "cuda":
+            raise ValueError("the weights must be on a CUDA device")
+        self.d, self.f, self.act, self.fmt = d, f, act, fmt
+        self.bank = dict(fmt=fmt, group=128, n_exp=1)
+        for m, N, K in (("gate", f, d), ("up", f, d), ("down", d, f)):
+            w = bank["w_" + m]
+            w = w[0] if w.dim() == 3 and w.shape[0] == 1 else w
+            int4 = fmt == "int4"
+            want = w.dtype if int4 and w.dtype in (torch.int32, torch.uint32) else \
+                torch.int32 if int4 else self.dtype
+            _check_rows(w, "w_" + m, N, K // 8 if int4 else K, want, self.device)
+            mats = [("w_" + m, w)]
+            if int4:
+                s = bank["s_" + m]
+                s = s[0] if s.dim() == 3 and s.shape[0] == 1 else s
+                _check_rows(s, "s_" + m, N, K // 128, torch.bfloat16, self.device)
+                mats.append(("s_" + m, s))
+            for name, t in mats:
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                self.bank[name] = t
+
+    def descriptor(self, T: int) -> MoeFfn:
+        """The descriptor of calls on T rows. It holds pointers into this object's tensors,
+        which must outlive it."""
+        F = MoeFfn(T, self.d, self.f, ACT_CODE[self.act], bank_struct(self.bank))
+        F.owner = self
+        _check(load_library().moe_ffn_validate(ctypes.byref(F)), "moe_ffn_validate")
+        return F
+
+
+def ffn_workspace_size(F: MoeFfn, backward: bool = False) -> int:
+    n = load_library().moe_ffn_workspace_size(ctypes.byref(F), int(backward))
+    if n == 0:
+        raise MoeError(-2, "moe_ffn_workspace_size")  # an int4 block has no backward pass
+    return n
+
+
+def alloc_ffn_workspace(F: MoeFfn, backward: bool = False):
+    """A zeroed workspace for ffn_forward, with ``backward`` for ffn_backward too."""
+    return _alloc_zeroed(ffn_workspace_size(F, backward), F.owner.device)
+
+
+def ffn_pre(F: MoeFfn, device=None):
+    """The fp32 tensor [2, T, f] in which ffn_forward keeps Wg x and Wu x for ffn_backward."""
+    import torch
+    return torch.empty((2, F.T, F.f), dtype=torch.float32, device=device or F.owner.device)
+
+
+def _check_pre(F: MoeFfn, pre):
+    import torch
+    if pre.dtype != torch.float32 or tuple(pre.shape) != (2, F.T, F.f) or \
+            pre.device != F.owner.device or not pre.is_contiguous():
+        raise ValueError(f"pre: expected contiguous fp32 [2, {F.T}, {F.f}] on {F.owner.device}")
+
+
+def _check_dense(F: MoeFfn, t, name, rows, cols):
+    if t.dtype != F.owner.dtype or t.device != F.owner.device or \
+            tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {F.owner.dtype} [{rows}, {cols}] on "
+                         f"{F.owner.device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
+    """y = Wd (act(Wg x) * (Wu x)) for the rows of x [T, d]; ``pre`` (ffn_pre) keeps what
+    ffn_backward needs (include/moe_b200.h)."""
+    import torch
+    dev = F.owner.device
+    _check_dense(F, x, "x", F.T, F.d)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check_dense(F, out, "out", F.T, F.d)
+    if pre is not None:
+        _check_pre(F, pre)
+    _check_ws(ws, dev)
+    _check(_call(dev, stream, load_library().moe_ffn_forward, ctypes.byref(F), x.data_ptr(),
+                 out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel()), "moe_ffn_forward")
+    return out
+
+
+def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool = True,
+                 stream=None):
+    """(dx, dw_gate, dw_up, dw_down) from dy [T, d], x and the ``pre`` of ffn_forward; what is
+    not needed is None and not computed. ``ws``: alloc_ffn_workspace(F, backward=True)."""
+    import torch
+    dev = F.owner.device
+    _check_dense(F, x, "x", F.T, F.d)
+    _check_dense(F, dy, "dy", F.T, F.d)
+    _check_pre(F, pre)
+    _check_ws(ws, dev)
+    dx = torch.empty_like(x) if need_dx else None
+    dwg = dwu = dwd = None
+    if need_dw:
+        dwg, dwu = (torch.empty((F.f, F.d), dtype=x.dtype, device=dev) for _ in range(2))
+        dwd = torch.empty((F.d, F.f), dtype=x.dtype, device=dev)
+    _check(_call(dev, stream, load_library().moe_ffn_backward, ctypes.byref(F), x.data_ptr(),
+                 dy.data_ptr(), pre.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd),
+                 ws.data_ptr(), ws.numel()), "moe_ffn_backward")
+    return dx, dwg, dwu, dwd
+
+
+def ffn_device_status(F: MoeFfn, ws, stream=None):
+    """(status code, wait site) kept in a block's workspace since the last read (0, 0: none)."""
+    code, site = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(_call(F.owner.device, stream, load_library().moe_ffn_device_status, ctypes.byref(F),
+                 ws.data_ptr(), ws.numel(), ctypes.byref(code), ctypes.byref(site)),
+           "moe_ffn_device_status")
+    return code.value, site.value

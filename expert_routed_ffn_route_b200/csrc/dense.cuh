@@ -87,4 +87,32 @@ struct GemvArgs {
 void gemv_scratch(const GemvArgs& a, size_t* partial_bytes, size_t* n_counters);
 cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool pdl);
 
+// ------------------------------------------------------------------ tensor-core kernels
+
+// A dense gated block on the tensor cores (dense_gemm.cu). 16-bit operands of one type.
+struct FfnArgs {
+  const void* w_gate;  // [f][d]
+  const void* w_up;    // [f][d]
+  const void* w_down;  // [d][f]
+  const void* x;       // [T][d]
+  void* h;             // [T][f]
+  float* pre;          // fp32 [2][T][f]: gate, then up, before the activation (or NULL)
+  void* y;             // [T][d]
+  const void* dy;      // [T][d]
+  void* dg;            // [T][f]
+  void* du;            // [T][f]
+  void* dx;            // [T][d] or NULL
+  void* dw_gate;       // [f][d] or NULL
+  void* dw_up;         // [f][d] or NULL
+  void* dw_down;       // [d][f] or NULL
+  int T, d, f, act;
+  bool f16;
+  int32_t* status;
+};
+
+cudaError_t launch_ffn_gate_up(const FfnArgs& a, cudaStream_t st);          // x -> h (and pre)
+cudaError_t launch_ffn_down(const FfnArgs& a, cudaStream_t st);             // h -> y
+cudaError_t launch_ffn_gate_grad(const FfnArgs& a, cudaStream_t st);        // dy, pre -> dg, du, h
+cudaError_t launch_ffn_grads(const FfnArgs& a, cudaStream_t st);            // -> dx and the weights'
+
 }  // namespace moe

@@ -21,7 +21,7 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // Whether [a, a + an) and [b, b + bn) share a byte.
 inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bn && y < x + an;
+  return a && b && an && bn && x < y + bn && y < x + an;
 }
 
 // ------------------------------------------------------------------ matvec
@@ -73,6 +73,135 @@ GemvWs gemv_ws(size_t partial_bytes, size_t n_counters) {
   return w;
 }
 
+// ------------------------------------------------------------------ dense gated block
+
+constexpr int kMaxWidth = 32768, kMaxFfnRows = 1 << 20;
+
+inline bool is_16bit(const moe_ffn* F) {
+  return F->bank.fmt == MOE_W_BF16 || F->bank.fmt == MOE_W_FP16;
+}
+
+moe_status ffn_validate(const moe_ffn* F) {
+  if (!F) return MOE_ERR_INVALID_ARG;
+  if (F->T < 1 || F->d < 1 || F->f < 1) return MOE_ERR_INVALID_ARG;
+  if (F->act != MOE_ACT_SILU && F->act != MOE_ACT_GELU) return MOE_ERR_INVALID_ARG;
+  const moe_bank& b = F->bank;
+  if (b.n_exp != 1) return MOE_ERR_INVALID_ARG;
+  if (!is_16bit(F) && b.fmt != MOE_W_INT4)
+    return b.fmt == MOE_W_INT8 || b.fmt == MOE_W_NVFP4 ? MOE_ERR_UNSUPPORTED
+                                                       : MOE_ERR_INVALID_ARG;
+  const int step = is_16bit(F) ? 8 : 128;
+  if (F->d % step || F->f % step) return MOE_ERR_INVALID_ARG;
+  if (F->d > kMaxWidth || F->f > kMaxWidth || F->T > kMaxFfnRows) return MOE_ERR_UNSUPPORTED;
+  for (const void* p : {b.w_gate, b.w_up, b.w_down})
+    if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (b.fmt == MOE_W_INT4) {
+    if (b.group != kGroup) return MOE_ERR_INVALID_ARG;
+    for (const void* p : {b.s_gate, b.s_up, b.s_down})
+      if (!p || !aligned(p, 2)) return MOE_ERR_INVALID_ARG;
+    if (F->T > kGemvMaxRows) return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+// Up to 32 rows the weights are streamed through the GEMV kernels; a call that keeps g and u
+// for a backward pass takes the tensor-core kernels at any T (they write them).
+inline bool streams(const moe_ffn* F, const void* pre) {
+  return !is_16bit(F) || (F->T <= kGemvMaxRows && !pre);
+}
+
+// Product i of the streamed block: 0 gate/up, 1 down.
+GemvArgs ffn_gemv(const moe_ffn* F, int i) {
+  GemvArgs a{};
+  const moe_bank& b = F->bank;
+  a.w[0] = i ? b.w_down : b.w_gate;
+  a.w[1] = i ? nullptr : b.w_up;
+  a.s[0] = static_cast<const uint16_t*>(i ? b.s_down : b.s_gate);
+  a.s[1] = static_cast<const uint16_t*>(i ? nullptr : b.s_up);
+  a.T = F->T;
+  a.N = i ? F->d : F->f;
+  a.K = i ? F->f : F->d;
+  a.ldx = a.K;
+  a.ldy = a.N;
+  a.fmt = is_16bit(F) ? 16 : 4;
+  a.group = kGroup;
+  a.f16 = b.fmt == MOE_W_FP16;
+  a.gated = !i;
+  a.act = F->act;
+  return a;
+}
+
+// Workspace of a block: the status block, the streaming kernels' counters and partial sums (the
+// two products run one after the other and share them), h, and for the backward pass dg, du.
+struct FfnWs {
+  GemvWs g;
+  size_t h, dg, du, total;
+};
+FfnWs ffn_ws(const moe_ffn* F, bool backward) {
+  FfnWs w;
+  size_t part = 0, cnt = 0;
+  if (F->T <= kGemvMaxRows)
+    for (int i = 0; i < 2; ++i) {
+      size_t p, c;
+      gemv_scratch(ffn_gemv(F, i), &p, &c);
+      part = std::max(part, p);
+      cnt = std::max(cnt, c);
+    }
+  w.g = gemv_ws(part, cnt);
+  const size_t rows = align_up((size_t)F->T * F->f * 2);
+  w.h = w.g.total;
+  w.dg = w.h + rows;
+  w.du = w.dg + (backward ? rows : 0);
+  w.total = w.du + (backward ? rows : 0);
+  return w;
+}
+
+moe_status ffn_check_ws(const moe_ffn* F, bool backward, const void* ws, size_t ws_bytes) {
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < ffn_ws(F, backward).total) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Whether one of the first n_out ranges (outputs) overlaps any other.
+bool outputs_overlap(const Range* r, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+
+inline size_t weight_bytes(const moe_ffn* F) {
+  const size_t n = (size_t)F->d * F->f;
+  return is_16bit(F) ? 2 * n : n / 2;
+}
+// Scales of one int4 matrix (0 when the bank has none, whatever its pointers hold).
+inline size_t scale_bytes(const moe_ffn* F) {
+  return is_16bit(F) ? 0 : (size_t)F->d * F->f / kGroup * 2;
+}
+
+FfnArgs ffn_args(const moe_ffn* F, void* ws, bool backward) {
+  const FfnWs w = ffn_ws(F, backward);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  FfnArgs a{};
+  a.w_gate = F->bank.w_gate;
+  a.w_up = F->bank.w_up;
+  a.w_down = F->bank.w_down;
+  a.h = base + w.h;
+  a.dg = base + w.dg;
+  a.du = base + w.du;
+  a.T = F->T;
+  a.d = F->d;
+  a.f = F->f;
+  a.act = F->act;
+  a.f16 = F->bank.fmt == MOE_W_FP16;
+  a.status = reinterpret_cast<int32_t*>(base);
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -107,6 +236,98 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   a.counters = reinterpret_cast<int32_t*>(base + w.counters);
   a.partial = reinterpret_cast<float*>(base + w.partial);
   MOE_TRY(launch_gemv_rows(a, reinterpret_cast<cudaStream_t>(stream), false));
+  return MOE_OK;
+}
+
+moe_status moe_ffn_validate(const moe_ffn* F) { return ffn_validate(F); }
+
+size_t moe_ffn_workspace_size(const moe_ffn* F, int32_t backward) {
+  if (ffn_validate(F) != MOE_OK || (backward && !is_16bit(F))) return 0;
+  return ffn_ws(F, backward != 0).total;
+}
+
+moe_status moe_ffn_forward(const moe_ffn* F, const void* x, void* y, float* pre, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  moe_status s = ffn_validate(F);
+  if (s != MOE_OK) return s;
+  if (pre && !is_16bit(F)) return MOE_ERR_UNSUPPORTED;
+  if (!x || !aligned(x, 16) || !y || !aligned(y, 16) || !aligned(pre, 16))
+    return MOE_ERR_INVALID_ARG;
+  if ((s = ffn_check_ws(F, false, ws, ws_bytes)) != MOE_OK) return s;
+  const size_t xb = (size_t)F->T * F->d * 2, wb = weight_bytes(F), sb = scale_bytes(F);
+  const moe_bank& b = F->bank;
+  const Range r[] = {{y, xb}, {pre, (size_t)F->T * F->f * 8}, {ws, ffn_ws(F, false).total}, {x, xb},
+                     {b.w_gate, wb}, {b.w_up, wb}, {b.w_down, wb}, {b.s_gate, sb}, {b.s_up, sb},
+                     {b.s_down, sb}};
+  if (outputs_overlap(r, 3, 10)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  FfnArgs a = ffn_args(F, ws, false);
+  if (streams(F, pre)) {
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const FfnWs w = ffn_ws(F, false);
+    for (int i = 0; i < 2; ++i) {
+      GemvArgs g = ffn_gemv(F, i);
+      g.x = static_cast<const uint16_t*>(i ? a.h : x);
+      g.y = i ? y : a.h;
+      g.counters = reinterpret_cast<int32_t*>(base + w.g.counters);
+      g.partial = reinterpret_cast<float*>(base + w.g.partial);
+      MOE_TRY(launch_gemv_rows(g, st, i == 1));
+    }
+    return MOE_OK;
+  }
+  a.x = x;
+  a.y = y;
+  a.pre = pre;
+  MOE_TRY(launch_ffn_gate_up(a, st));
+  MOE_TRY(launch_ffn_down(a, st));
+  return MOE_OK;
+}
+
+moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void* dy, const float* pre,
+                            void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+  moe_status s = ffn_validate(F);
+  if (s != MOE_OK) return s;
+  if (!is_16bit(F)) return MOE_ERR_UNSUPPORTED;
+  for (const void* p : {x, dy, static_cast<const void*>(pre)})
+    if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {dx, dw_gate, dw_up, dw_down})
+    if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_ERR_INVALID_ARG;
+  if ((s = ffn_check_ws(F, true, ws, ws_bytes)) != MOE_OK) return s;
+  const size_t xb = (size_t)F->T * F->d * 2, wb = weight_bytes(F);
+  const moe_bank& b = F->bank;
+  const Range r[] = {{dx, xb}, {dw_gate, wb}, {dw_up, wb}, {dw_down, wb},
+                     {ws, ffn_ws(F, true).total}, {x, xb}, {dy, xb},
+                     {pre, (size_t)F->T * F->f * 8}, {b.w_gate, wb}, {b.w_up, wb}, {b.w_down, wb}};
+  if (outputs_overlap(r, 5, 11)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  FfnArgs a = ffn_args(F, ws, true);
+  a.x = x;
+  a.dy = dy;
+  a.pre = const_cast<float*>(pre);
+  a.dx = dx;
+  a.dw_gate = dw_gate;
+  a.dw_up = dw_up;
+  a.dw_down = dw_down;
+  MOE_TRY(launch_ffn_gate_grad(a, st));
+  MOE_TRY(launch_ffn_grads(a, st));
+  return MOE_OK;
+}
+
+moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes, int32_t* code,
+                                 int32_t* site, moe_stream_t stream) {
+  moe_status s = ffn_validate(F);
+  if (s != MOE_OK) return s;
+  if (!code || !site) return MOE_ERR_INVALID_ARG;
+  if ((s = ffn_check_ws(F, false, ws, ws_bytes)) != MOE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int32_t words[kSiteWord + 1] = {};
+  MOE_TRY(cudaMemcpyAsync(words, ws, sizeof(words), cudaMemcpyDeviceToHost, st));
+  MOE_TRY(cudaStreamSynchronize(st));
+  MOE_TRY(cudaMemsetAsync(ws, 0, sizeof(words), st));
+  *code = words[0] == DEV_OK ? MOE_OK : words[0] == DEV_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_ERR_DEVICE;
+  *site = words[kSiteWord];
   return MOE_OK;
 }
 

@@ -88,7 +88,8 @@ typedef enum {
   MOE_ERR_TOO_LARGE = -7    /* the request needs more than the library's built-in scratch */
 } moe_status;
 
-typedef enum { MOE_W_BF16 = 16, MOE_W_INT8 = 8, MOE_W_INT4 = 4, MOE_W_NVFP4 = 41 } moe_wfmt;
+typedef enum { MOE_W_BF16 = 16, MOE_W_INT8 = 8, MOE_W_INT4 = 4, MOE_W_NVFP4 = 41,
+               MOE_W_FP16 = 17 /* the dense block only (moe_ffn) */ } moe_wfmt;
 
 /* Element types of the dense operators' activations and results. */
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
@@ -328,6 +329,55 @@ MOE_API size_t moe_matvec_workspace_size(const moe_matrix* M);
 /* y = x W^T (+ bias), one kernel. x [T][ldx], y [T][ldy]. */
 MOE_API moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws,
                               size_t ws_bytes, moe_stream_t stream);
+
+/* A dense gated feed-forward block, forward and backward:
+ *   g = Wg x, u = Wu x, h = act(g) * u, y = Wd h            (rows x [T][d] -> y [T][d])
+ *   dh = Wd^T dy, du = dh act(g), dg = dh u act'(g),
+ *   dx = Wg^T dg + Wu^T du, dWg = dg x^T, dWu = du x^T, dWd = dy h^T   (sums over the rows)
+ * bank holds the three matrices as a bank of one expert (n_exp = 1; w_gate, w_up [f][d], w_down
+ * [d][f]) in one of
+ *   MOE_W_BF16, MOE_W_FP16  plain 16-bit values; x, y and every gradient have that type.
+ *                           d and f multiples of 8 (8..32768), 1 <= T <= 2^20.
+ *   MOE_W_INT4              group 128 (d and f multiples of 128); x, y bf16; forward only, up
+ *                           to 32 rows (MOE_ERR_UNSUPPORTED beyond).
+ * Products are summed in fp32; h, dg and du are rounded to the 16-bit type (the next product's
+ * operand: an h, dg or du beyond fp16's 65504 becomes infinite), g and u are kept in fp32, dh is
+ * never stored. Every pointer is 16-byte aligned (int4 scales: 2) and rows are dense. Outputs
+ * must not overlap each other or an input. */
+typedef struct {
+  int32_t T, d, f;
+  int32_t act; /* moe_act */
+  moe_bank bank;
+} moe_ffn;
+
+/* Host-side validation of a block descriptor (no CUDA call is made). */
+MOE_API moe_status moe_ffn_validate(const moe_ffn* F);
+
+/* Bytes of device workspace of moe_ffn_forward (backward == 0) or of both calls (backward != 0;
+ * 0 for an int4 block, which has no backward pass); 0 if F is invalid. Rules as for
+ * moe_matvec_workspace_size. */
+MOE_API size_t moe_ffn_workspace_size(const moe_ffn* F, int32_t backward);
+
+/* y from x. pre: fp32 [2][T][f], receives g, then u, for the backward pass; NULL when none
+ * follows (required NULL for int4). Calls of up to 32 rows without pre stream the weights
+ * (two kernels); others run on the tensor cores (two kernels), in another order of sums. */
+MOE_API moe_status moe_ffn_forward(const moe_ffn* F, const void* x, void* y, float* pre, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+
+/* Gradients from dy [T][d], x and the pre that moe_ffn_forward wrote for the same x and weights
+ * (two kernels). dx [T][d], dw_gate, dw_up [f][d], dw_down [d][f] are overwritten, each may be
+ * NULL (not computed) but not all of them. The result does not depend on the order of
+ * execution: no atomics. The workspace keeps nothing from the forward pass. */
+MOE_API moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void* dy,
+                                    const float* pre, void* dx, void* dw_gate, void* dw_up,
+                                    void* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Reads the status word of a block's workspace (synchronises `stream`), writes MOE_OK,
+ * MOE_ERR_TIMEOUT or MOE_ERR_DEVICE to *code and the site of the bounded wait that gave up to
+ * *site (0: none; 50 stage free, 51 stage landed or accumulator free, 52 accumulator full),
+ * and clears both. */
+MOE_API moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes,
+                                         int32_t* code, int32_t* site, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

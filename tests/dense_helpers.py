@@ -58,3 +58,76 @@ def assert_close(got, ref, bound, dtype, what=""):
     ratio = ((got - ref).abs() / tol).max().item() if bad.numel() else 0.0
     assert worst <= 0, f"{what}: {ratio:.3f} of the bound"
     return ratio
+
+
+# ---------------------------------------------------------------------- dense gated block
+
+ACT_LIPSCHITZ = 1.13   # max |act'| of silu (1.10) and gelu (1.13)
+ACT2_LIPSCHITZ = 1.2   # max |act''| of silu (0.5) and tanh gelu (1.13)
+FUNC = 2.0 ** -18      # relative error of the kernels' fp32 activations (fast exponential,
+                       # |g| < 64: its argument's rounding, 64 * 2^-24 relative)
+
+
+def activation(g, act):
+    """act(g), act'(g) in the tensors' precision."""
+    if act == "silu":
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s))
+    c = (2 / torch.pi) ** 0.5
+    t = torch.tanh(c * (g + 0.044715 * g ** 3))
+    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+
+
+def additions(K):
+    """Additions of a K-long tensor-core product, at most: two per step of 16, and the partial
+    sums of split products."""
+    return K // 8 + 64
+
+
+def ffn_ref(x, wg, wu, wd, act, dtype, dy=None):
+    """{name: (value in 64 bits, bound of a kernel's error before the result's own rounding)}:
+    fp32 sums, h, dg and du rounded to dtype, g and u kept in fp32."""
+    half, tiny = HALF_STEP[dtype], TINY[dtype]
+    x, wg, wu, wd = (t.double() for t in (x, wg, wu, wd))
+    T, d = x.shape
+    f = wg.shape[0]
+    u32 = 2.0 ** -23
+    g, u = x @ wg.T, x @ wu.T
+    eg = (x.abs() @ wg.abs().T) * additions(d) * u32
+    eu = (x.abs() @ wu.abs().T) * additions(d) * u32
+    a, da = activation(g, act)
+    h = a * u
+    ea = ACT_LIPSCHITZ * eg + FUNC * (a.abs() + g.abs())
+    eh = ea * u.abs() + a.abs() * eu + ea * eu
+    eh = eh + half * (h.abs() + eh) + tiny
+    out = {"y": (h @ wd.T, eh @ wd.abs().T + additions(f) * u32 * ((h.abs() + eh) @ wd.abs().T))}
+    if dy is None:
+        return out
+    dy = dy.double()
+    dh = dy @ wd
+    edh = (dy.abs() @ wd.abs()) * additions(d) * u32
+    dg, du = dh * u * da, dh * a
+    eda = ACT2_LIPSCHITZ * eg + FUNC * (1 + g.abs())
+    edg = edh * (u * da).abs() + dh.abs() * (eu * da.abs() + u.abs() * eda) + u32 * dg.abs()
+    edu = edh * a.abs() + dh.abs() * ea + u32 * du.abs()
+    edg = 1.01 * edg + half * (dg.abs() + edg) + tiny   # 1.01: the products of two errors
+    edu = 1.01 * edu + half * (du.abs() + edu) + tiny
+    mg, mu, mh = dg.abs() + edg, du.abs() + edu, h.abs() + eh
+    out["dx"] = (dg @ wg + du @ wu, edg @ wg.abs() + edu @ wu.abs() +
+                 additions(2 * f) * u32 * (mg @ wg.abs() + mu @ wu.abs()))
+    n = additions(T) * u32
+    out["dw_gate"] = (dg.T @ x, edg.T @ x.abs() + n * (mg.T @ x.abs()))
+    out["dw_up"] = (du.T @ x, edu.T @ x.abs() + n * (mu.T @ x.abs()))
+    out["dw_down"] = (dy.T @ h, dy.abs().T @ eh + n * (dy.abs().T @ mh))
+    return out
+
+
+def assert_norm_close(got, ref, dtype, what=""):
+    """Relative error in the 2-norm: at most three roundings to dtype lie between the inputs and
+    a result, each off by at most half a step of every value, independent of one another; a
+    fourth is left for the fp32 sums. Catches a term that is missing or counted twice, which
+    the worst-case bounds of long sums could hide."""
+    got, ref = got.double(), ref.to(got.device)
+    rel = ((got - ref).norm() / ref.norm().clamp_min(1e-300)).item()
+    assert rel <= 4 * HALF_STEP[dtype], f"{what}: {rel:.3e}"
+    return rel

@@ -97,3 +97,110 @@ def test_binding_refuses_tensors_that_do_not_fit():
     for t in (x[:, ::2], x.T, x.float(), x[:3], x[:1].expand(4, 8)):
         with pytest.raises(ValueError):
             binding._check_rows(t, "x", 4, 8, torch.bfloat16, dev)
+
+
+def ffn(fmt=16, **kw):
+    bank = binding.MoeBank(fmt, 128, 1, 0, *([FAKE] * 6), None, None, None)
+    F = binding.MoeFfn(40, 2560, 1024, 0, bank)
+    for k, v in kw.items():
+        setattr(F.bank if k.startswith("w_") or k.startswith("s_") or
+                k in ("fmt", "group", "n_exp") else F, k, v)
+    return F
+
+
+@pytest.mark.parametrize("fields,code", [
+    ({}, 0), ({"fmt": 17}, 0), ({"act": 1}, 0), ({"d": 8, "f": 8}, 0), ({"T": 1}, 0),
+    ({"fmt": 4, "T": 32}, 0), ({"s_gate": None, "s_up": None, "s_down": None}, 0),
+    ({"T": 1 << 20, "d": 32768, "f": 32768}, 0),
+    ({"T": 0}, -1), ({"T": (1 << 20) + 1}, -2), ({"d": 4}, -1), ({"d": 12}, -1), ({"f": 0}, -1),
+    ({"d": 32776}, -2), ({"f": 40000}, -2), ({"act": 2}, -1), ({"n_exp": 2}, -1), ({"n_exp": 0}, -1),
+    ({"fmt": 4, "T": 33}, -2), ({"fmt": 4, "T": 4, "d": 192}, -1),
+    ({"fmt": 4, "T": 4, "group": 64}, -1), ({"fmt": 4, "T": 4, "s_up": None}, -1),
+    ({"fmt": 8}, -2), ({"fmt": 41}, -2), ({"fmt": 3}, -1), ({"w_up": None}, -1),
+    ({"w_down": FAKE + 8}, -1),
+])
+def test_ffn_validation(lib, fields, code):
+    F = ffn(**fields)
+    assert lib.moe_ffn_validate(ctypes.byref(F)) == code
+    fwd = lib.moe_ffn_workspace_size(ctypes.byref(F), 0)
+    both = lib.moe_ffn_workspace_size(ctypes.byref(F), 1)
+    if code == 0:
+        assert fwd >= 256 + 2 * F.T * F.f and fwd % 256 == 0
+        assert both == 0 if F.bank.fmt == 4 else both >= fwd + 4 * F.T * F.f
+    else:
+        assert fwd == 0 and both == 0
+
+
+def test_ffn_calls_reject_bad_arguments_before_any_cuda_call(lib):
+    F = ffn()
+    p = [(i + 2) << 36 for i in range(12)]
+    F.bank.w_gate, F.bank.w_up, F.bank.w_down = p[:3]
+    x, y, pre, ws, dy, dx, dwg, dwu, dwd = p[3:]
+    big = 1 << 34
+    fw = lambda **k: lib.moe_ffn_forward(  # noqa: E731
+        ctypes.byref(k.get("F", F)), k.get("x", x), k.get("y", y), k.get("pre", None),
+        k.get("ws", ws), k.get("n", big), None)
+    for bad in ({"x": None}, {"y": None}, {"x": x + 8}, {"y": y + 2}, {"pre": pre + 4}, {"y": x},
+                {"y": p[0] + 64}, {"pre": x}, {"ws": x}, {"y": ws}):
+        assert fw(**bad) == -1, bad
+    assert fw(ws=None) == -5 and fw(ws=ws + 16) == -5 and fw(n=1000) == -5
+    q = ffn(fmt=4, T=4)
+    assert fw(F=q, pre=pre) == -2
+    bw = lambda **k: lib.moe_ffn_backward(  # noqa: E731
+        ctypes.byref(k.get("F", F)), k.get("x", x), k.get("dy", dy), k.get("pre", pre),
+        k.get("dx", dx), k.get("dwg", dwg), k.get("dwu", dwu), k.get("dwd", dwd),
+        k.get("ws", ws), k.get("n", big), None)
+    for bad in ({"x": None}, {"dy": None}, {"pre": None}, {"dx": dx + 8}, {"dwd": dwd + 2},
+                {"dx": None, "dwg": None, "dwu": None, "dwd": None}, {"dx": dy}, {"dwg": dwu},
+                {"dwd": p[2]}, {"dwu": pre}, {"ws": pre}):
+        assert bw(**bad) == -1, bad
+    assert bw(ws=None) == -5
+    assert bw(n=lib.moe_ffn_workspace_size(ctypes.byref(F), 0)) == -5
+    assert bw(F=q) == -2
+    code = ctypes.c_int32(0)
+    assert lib.moe_ffn_device_status(ctypes.byref(F), ws, big, None, ctypes.byref(code), None) == -1
+
+
+def test_reference_gradients_match_autograd_and_differences():
+    """The plain implementation the GPU tests compare with: its gradient formulas against
+    automatic differentiation and against central differences, in 64 bits."""
+    torch = pytest.importorskip("torch")
+    from dense_helpers import ffn_ref
+    torch.manual_seed(0)
+    for act in ("silu", "gelu"):
+        T, d, f = 5, 8, 16
+        x, wg, wu, wd, dy = (torch.randn(*s, dtype=torch.float64)
+                             for s in ((T, d), (f, d), (f, d), (d, f), (T, d)))
+        ref = ffn_ref(x, wg, wu, wd, act, torch.bfloat16, dy=dy)
+        leaves = [t.clone().requires_grad_() for t in (x, wg, wu, wd)]
+        F = torch.nn.functional
+        act_fn = F.silu if act == "silu" else (lambda t: F.gelu(t, approximate="tanh"))
+
+        def fwd(v):
+            return F.linear(act_fn(F.linear(v[0], v[1])) * F.linear(v[0], v[2]), v[3])
+        y = fwd(leaves)
+        torch.testing.assert_close(ref["y"][0], y.detach(), rtol=1e-12, atol=1e-12)
+        names = ("dx", "dw_gate", "dw_up", "dw_down")
+        for i, (n, g) in enumerate(zip(names, torch.autograd.grad(y, leaves, dy))):
+            torch.testing.assert_close(ref[n][0], g, rtol=1e-11, atol=1e-11)
+            v = torch.randn_like(g)
+            e, base = 1e-6, [t.detach() for t in leaves]
+            plus, minus = ((fwd([t + s * e * v if j == i else t for j, t in enumerate(base)]) * dy).sum()
+                           for s in (1, -1))
+            diff, dot = (plus - minus) / (2 * e), (g * v).sum()
+            assert abs(diff - dot) <= 1e-7 * (1 + dot.abs()), n
+
+
+def test_ffn_struct_layout_matches_the_header(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "abi.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "moe_b200.h"\n'
+                   'int main(void) { printf("%zu %zu\\n", sizeof(moe_ffn), offsetof(moe_ffn, bank));'
+                   ' return 0; }\n')
+    exe = tmp_path / "abi"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror",
+                    "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    sizes = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                            check=True).stdout.split()]
+    assert sizes == [ctypes.sizeof(binding.MoeFfn), binding.MoeFfn.bank.offset]

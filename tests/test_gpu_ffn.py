@@ -1,0 +1,308 @@
+"""The dense gated block on the GPU, forward and backward, against a plain implementation in 64
+bits and against differences."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from dense_helpers import (TINY, activation, assert_close, assert_norm_close, dequantise, ffn_ref,
+                           matvec_additions, matvec_ref, quantise)
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+FMT = {BF: "bf16", HF: "fp16"}
+
+
+@pytest.fixture(scope="module")
+def B():
+    from expert_routed_ffn_route_b200 import binding
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    binding.load_library()
+    return binding
+
+
+def make(B, d, f, dtype=BF, act="silu", seed=0, fmt=None):
+    """A block on the GPU and its weights in 64 bits."""
+    gen = torch.Generator().manual_seed(seed)
+    bank, W = dict(fmt=fmt or FMT[dtype], group=128, n_exp=1), []
+    for m, N, K in (("gate", f, d), ("up", f, d), ("down", d, f)):
+        if fmt == "int4":
+            codes, scales = quantise(gen, N, K, 128)
+            bank["w_" + m], bank["s_" + m] = codes.cuda(), scales.cuda()
+            W.append(dequantise(codes, scales, 128).cuda())
+        else:
+            w = (torch.randn(N, K, generator=gen) * K ** -0.5).to(dtype).cuda()
+            bank["w_" + m] = w
+            W.append(w.double())
+    return B.DeviceFfn(bank, d, f, act=act), W
+
+
+def rows(T, d, dtype, seed=1, scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, d, generator=gen) * scale).to(dtype).cuda()
+
+
+def guarded(T, cols, dtype):
+    """[T, cols] inside a larger buffer whose rest must stay as it was."""
+    buf = torch.full((T * cols + 256,), 3.0, dtype=dtype, device="cuda")
+    return buf, buf[:T * cols].view(T, cols)
+
+
+# T, d, f: single rows and values, tails in every direction of the 128 x (64, 128, 256) x 64 tiles
+SHAPES = [
+    (1, 8, 8), (1, 128, 256), (2, 264, 72), (7, 136, 520), (31, 1024, 264), (32, 512, 1032),
+    (33, 8, 16), (33, 136, 72), (64, 2560, 1024), (100, 72, 2056), (127, 64, 64),
+    (128, 128, 128), (129, 256, 264), (257, 1032, 136), (300, 520, 1032), (700, 1288, 1160),
+    (2049, 640, 392),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,d,f", SHAPES)
+def test_forward_matches_64_bits(B, T, d, f, act, dtype):
+    block, W = make(B, d, f, dtype, act, seed=d + f)
+    x = rows(T, d, dtype)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc)
+    buf, y = guarded(T, d, dtype)
+    B.ffn_forward(desc, x, ws, out=y)
+    pbuf, pre = guarded(2 * T, f, F32)
+    pre = pre.view(2, T, f)
+    y2 = B.ffn_forward(desc, x, ws, pre=pre)
+    assert B.ffn_device_status(desc, ws) == (0, 0)
+    ref, bound = ffn_ref(x, *W, act, dtype)["y"]
+    for out in (y, y2):
+        assert_close(out, ref, bound, dtype, "y")
+        assert_norm_close(out, ref, dtype, "y")
+    assert (buf[T * d:] == 3).all() and (pbuf[2 * T * f:] == 3).all()
+    xd = x.double()
+    for got, w in zip(pre, W[:2]):
+        r, mag = matvec_ref(xd, w)
+        assert_close(got, r, mag * (d // 8 + 64) * 2.0 ** -23, F32, "pre")
+    if T > 32:  # the same kernels with and without pre
+        assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype,act", [(BF, "silu"), (HF, "gelu"), (BF, "gelu"), (HF, "silu")])
+@pytest.mark.parametrize("T,d,f", SHAPES)
+def test_backward_matches_64_bits(B, T, d, f, act, dtype):
+    block, W = make(B, d, f, dtype, act, seed=d + f + 1)
+    x, dy = rows(T, d, dtype), rows(T, d, dtype, seed=2, scale=0.5)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc, backward=True)
+    pre = B.ffn_pre(desc)
+    B.ffn_forward(desc, x, ws, pre=pre)
+    names = ("dx", "dw_gate", "dw_up", "dw_down")
+    got = dict(zip(names, B.ffn_backward(desc, x, dy, pre, ws)))
+    again = dict(zip(names, B.ffn_backward(desc, x, dy, pre, ws)))
+    assert B.ffn_device_status(desc, ws) == (0, 0)
+    ref = ffn_ref(x, *W, act, dtype, dy=dy)
+    for n in names:
+        assert torch.equal(got[n], again[n]), n
+        assert_close(got[n], *ref[n], dtype, n)
+        assert_norm_close(got[n], ref[n][0], dtype, n)
+
+
+def test_only_what_is_asked_for_is_computed(B):
+    T, d, f = 200, 136, 264
+    block, W = make(B, d, f)
+    x, dy = rows(T, d, BF), rows(T, d, BF, seed=2)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc, backward=True)
+    pre = B.ffn_pre(desc)
+    B.ffn_forward(desc, x, ws, pre=pre)
+    full = B.ffn_backward(desc, x, dy, pre, ws)
+    dx, *none = B.ffn_backward(desc, x, dy, pre, ws, need_dw=False)
+    assert none == [None] * 3 and torch.equal(dx, full[0])
+    none, *dws = B.ffn_backward(desc, x, dy, pre, ws, need_dx=False)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(dws, full[1:]))
+    with pytest.raises(B.MoeError):
+        B.ffn_backward(desc, x, dy, pre, ws, need_dx=False, need_dw=False)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_match_differences(B, act):
+    """<gradient, direction> against central differences of the 64-bit forward pass: step e
+    gives a truncation error of order e^2 and a rounding error of order 2^-52 / e, both below
+    1e-9; what remains is the kernels' 16-bit rounding, bounded by the gradient's own."""
+    T, d, f = 96, 136, 200
+    block, W = make(B, d, f, HF, act)
+    x, dy = rows(T, d, HF), rows(T, d, HF, seed=2)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc, backward=True)
+    pre = B.ffn_pre(desc)
+    B.ffn_forward(desc, x, ws, pre=pre)
+    grads = B.ffn_backward(desc, x, dy, pre, ws)
+    inputs = [x.double()] + W
+
+    def loss(v):
+        g, u = v[0] @ v[1].T, v[0] @ v[2].T
+        return ((activation(g, act)[0] * u) @ v[3].T * dy.double()).sum()
+
+    ref = ffn_ref(x, *W, act, HF, dy=dy)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    for i, (name, grad) in enumerate(zip(("dx", "dw_gate", "dw_up", "dw_down"), grads)):
+        v = torch.randn(grad.shape, generator=gen, device="cuda", dtype=torch.float64)
+        e = 1e-5
+        plus, minus = (loss([t + s * e * v if j == i else t for j, t in enumerate(inputs)])
+                       for s in (1, -1))
+        diff = ((plus - minus) / (2 * e)).item()
+        tol = ((ref[name][1] + grad.double().abs() * 2.0 ** -11 + TINY[HF]) * v.abs()).sum().item()
+        assert abs((grad.double() * v).sum().item() - diff) <= tol + 1e-6 * abs(diff), name
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,d,f", [(1, 128, 128), (1, 2560, 1024), (3, 256, 384), (8, 640, 256),
+                                   (9, 384, 1280), (16, 2560, 512), (17, 128, 2560),
+                                   (32, 2560, 2560)])
+def test_int4_block_matches_64_bits(B, T, d, f, act):
+    block, W = make(B, d, f, fmt="int4", act=act, seed=d + f)
+    x = rows(T, d, BF)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc)
+    buf, y = guarded(T, d, BF)
+    B.ffn_forward(desc, x, ws, out=y)
+    assert torch.equal(y, B.ffn_forward(desc, x, ws))
+    ref, bound = ffn_ref(x, *W, act, BF)["y"]
+    assert_close(y, ref, bound, BF, "y")
+    assert_norm_close(y, ref, BF, "y")
+    assert (buf[T * d:] == 3).all()
+
+
+def test_gates_far_from_zero(B):
+    """Saturated gates: silu and gelu give g or 0 (never NaN), their slopes 1 or 0."""
+    T, d, f = 64, 64, 64
+    for act in ("silu", "gelu"):
+        block, W = make(B, d, f, BF, act)
+        x = rows(T, d, BF, scale=3e4)
+        dy = rows(T, d, BF, seed=2)
+        desc = block.descriptor(T)
+        ws = B.alloc_ffn_workspace(desc, backward=True)
+        pre = B.ffn_pre(desc)
+        y = B.ffn_forward(desc, x, ws, pre=pre)
+        grads = B.ffn_backward(desc, x, dy, pre, ws)
+        g, u = pre[0].double(), pre[1].double()
+        sat = g.abs() > 100
+        assert sat.float().mean() > 0.9
+        for t in (y, *grads):
+            assert torch.isfinite(t).all()
+        a, da = g.clamp_min(0), (g > 0).double()
+        h = torch.where(sat, a * u, activation(g, act)[0] * u)
+        assert_norm_close(y, h @ W[2].T, BF, act)
+        dh = dy.double() @ W[2]
+        slope = torch.where(sat, da, activation(g, act)[1])
+        act_v = torch.where(sat, a, activation(g, act)[0])
+        assert_norm_close(grads[1], (dh * u * slope).T @ x.double(), BF, act)
+        assert_norm_close(grads[2], (dh * act_v).T @ x.double(), BF, act)
+
+
+@pytest.mark.parametrize("T", [1, 20, 200])
+def test_a_nan_row_stays_alone(B, T):
+    block, W = make(B, 256, 384)
+    x = rows(T, 256, BF)
+    x[T // 2, 5] = float("nan")
+    desc = block.descriptor(T)
+    y = B.ffn_forward(desc, x, B.alloc_ffn_workspace(desc))
+    assert torch.isnan(y[T // 2]).all()
+    keep = [t for t in range(T) if t != T // 2]
+    if keep:
+        ref, bound = ffn_ref(x[keep], *W, "silu", BF)["y"]
+        assert_close(y[keep], ref, bound, BF)
+
+
+def test_captured_step_replayed_beside_another(B):
+    """A training step captured into a graph, two of them with their own workspaces replayed at
+    once on two streams."""
+    T, d, f = 150, 264, 392
+    steps = []
+    for seed in (1, 2):
+        block, W = make(B, d, f, seed=seed)
+        x, dy = rows(T, d, BF, seed), rows(T, d, BF, seed + 10)
+        desc = block.descriptor(T)
+        c = dict(desc=desc, block=block, W=W, x=x, dy=dy, s=torch.cuda.Stream(), g=torch.cuda.CUDAGraph(),
+                 ws=B.alloc_ffn_workspace(desc, backward=True), pre=B.ffn_pre(desc))
+
+        def step(c=c):
+            c["y"] = B.ffn_forward(c["desc"], c["x"], c["ws"], pre=c["pre"])
+            c["grads"] = B.ffn_backward(c["desc"], c["x"], c["dy"], c["pre"], c["ws"])
+        step()
+        torch.cuda.synchronize()
+        c["eager"] = [t.clone() for t in (c["y"], *c["grads"])]
+        with torch.cuda.graph(c["g"], stream=c["s"]):
+            step()
+        steps.append(c)
+    for _ in range(10):
+        for c in steps:
+            with torch.cuda.stream(c["s"]):
+                c["g"].replay()
+    torch.cuda.synchronize()
+    for c in steps:
+        for a, b in zip((c["y"], *c["grads"]), c["eager"]):
+            assert torch.equal(a, b)
+        assert B.ffn_device_status(c["desc"], c["ws"]) == (0, 0)
+
+
+def test_refusals(B):
+    block, _ = make(B, 128, 128)
+    int4, _ = make(B, 128, 128, fmt="int4")
+    with pytest.raises(B.MoeError):
+        int4.descriptor(33)
+    d4 = int4.descriptor(4)
+    with pytest.raises(B.MoeError):
+        B.alloc_ffn_workspace(d4, backward=True)
+    x = rows(4, 128, BF)
+    with pytest.raises(B.MoeError):
+        B.ffn_forward(d4, x, B.alloc_ffn_workspace(d4), pre=B.ffn_pre(d4))
+    desc = block.descriptor(4)
+    ws = B.alloc_ffn_workspace(desc)
+    with pytest.raises(B.MoeError):  # a forward workspace is too small for the backward pass
+        B.ffn_backward(desc, x, x, B.ffn_pre(desc), ws)
+    for bad in (x.half(), x[:3], x.cpu(), rows(4, 256, BF)[:, ::2]):
+        with pytest.raises(ValueError):
+            B.ffn_forward(desc, bad, ws)
+    with pytest.raises(B.MoeError):  # in place
+        B.ffn_forward(desc, x, ws, out=x)
+    with pytest.raises(ValueError):
+        make(B, 132, 128)
+
+
+def test_layer_block_and_projection_in_one_captured_step(B):
+    """A decode step as a model runs it: the routed layer, a dense int4 block on its output, and
+    the vocabulary projection, captured together; each stage against its own reference on the
+    stage's actual input."""
+    from expert_routed_ffn_route_b200 import synth
+    T, V = 4, 1003
+    cfg = synth.LayerConfig("run", T=T, d=256, E=16, k=2, f=128, fmt="int4", seed=3)
+    L = synth.make_layer(cfg)
+    dl = B.DeviceLayer(L)
+    ld = dl.descriptor(T)
+    lws = B.alloc_workspace(ld)
+    block, W = make(B, 256, 512, fmt="int4")
+    bd = block.descriptor(T)
+    bws = B.alloc_ffn_workspace(bd)
+    gen = torch.Generator().manual_seed(9)
+    codes, scales = quantise(gen, V, 256, 64)
+    proj = B.QuantMatrix(codes.cuda(), scales.cuda(), 256, 64)
+    pd = proj.descriptor(T, y_dtype=F32)
+    pws = B.alloc_matvec_workspace(pd)
+    x = torch.from_numpy(L.x.view("int16")).cuda().view(BF)
+
+    def step():
+        a = B.layer_forward(ld, x, lws)
+        b = B.ffn_forward(bd, a, bws)
+        return a, b, B.matvec(pd, b, pws)
+    eager = [t.clone() for t in step()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, eager):
+        assert torch.equal(a, b)
+    assert B.device_status(ld, lws) == 0
+    ref, bound = ffn_ref(out[0], *W, "silu", BF)["y"]
+    assert_close(out[1], ref, bound, BF, "block")
+    ref, mag = matvec_ref(out[1].cpu(), dequantise(codes, scales, 64))
+    assert_close(out[2], ref, mag * matvec_additions(256, 64) * 2.0 ** -23, F32, "projection")
