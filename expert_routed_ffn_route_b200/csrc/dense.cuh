@@ -108,7 +108,14 @@ struct FfnArgs {
   int T, d, f, act;
   bool f16;
   int32_t* status;
+  float* partial;      // sums of tiles split along K
+  size_t partial_bytes;
+  int32_t* counters;   // ffn_counters() of them, zero between calls
 };
+
+// Workspace of the tensor-core kernels: bytes of partial sums, number of counters.
+size_t ffn_partial_bytes(const FfnArgs& a, bool backward);
+size_t ffn_counters();
 
 cudaError_t launch_ffn_gate_up(const FfnArgs& a, cudaStream_t st);          // x -> h (and pre)
 cudaError_t launch_ffn_down(const FfnArgs& a, cudaStream_t st);             // h -> y

@@ -131,12 +131,22 @@ GemvArgs ffn_gemv(const moe_ffn* F, int i) {
   return a;
 }
 
-// Workspace of a block: the status block, the streaming kernels' counters and partial sums (the
-// two products run one after the other and share them), h, and for the backward pass dg, du.
+// Workspace of a block: the status block, counters and partial sums (of the streaming kernels or
+// the tensor-core kernels; a call's products run one after the other and share them), h, and
+// for the backward pass dg, du.
 struct FfnWs {
   GemvWs g;
-  size_t h, dg, du, total;
+  size_t partial_bytes, h, dg, du, total;
 };
+FfnArgs ffn_shape(const moe_ffn* F) {
+  FfnArgs a{};
+  a.T = F->T;
+  a.d = F->d;
+  a.f = F->f;
+  a.act = F->act;
+  a.f16 = F->bank.fmt == MOE_W_FP16;
+  return a;
+}
 FfnWs ffn_ws(const moe_ffn* F, bool backward) {
   FfnWs w;
   size_t part = 0, cnt = 0;
@@ -147,7 +157,14 @@ FfnWs ffn_ws(const moe_ffn* F, bool backward) {
       part = std::max(part, p);
       cnt = std::max(cnt, c);
     }
+  if (is_16bit(F)) {
+    const FfnArgs a = ffn_shape(F);
+    part = std::max(part, ffn_partial_bytes(a, false));
+    if (backward) part = std::max(part, ffn_partial_bytes(a, true));
+    cnt = std::max(cnt, ffn_counters());
+  }
   w.g = gemv_ws(part, cnt);
+  w.partial_bytes = part;
   const size_t rows = align_up((size_t)F->T * F->f * 2);
   w.h = w.g.total;
   w.dg = w.h + rows;
@@ -156,9 +173,8 @@ FfnWs ffn_ws(const moe_ffn* F, bool backward) {
   return w;
 }
 
-moe_status ffn_check_ws(const moe_ffn* F, bool backward, const void* ws, size_t ws_bytes) {
-  if (!ws || !aligned(ws, kAlign) || ws_bytes < ffn_ws(F, backward).total) return MOE_ERR_WORKSPACE;
-  return MOE_OK;
+moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  return ws && aligned(ws, kAlign) && ws_bytes >= need ? MOE_OK : MOE_ERR_WORKSPACE;
 }
 
 struct Range {
@@ -183,22 +199,19 @@ inline size_t scale_bytes(const moe_ffn* F) {
   return is_16bit(F) ? 0 : (size_t)F->d * F->f / kGroup * 2;
 }
 
-FfnArgs ffn_args(const moe_ffn* F, void* ws, bool backward) {
-  const FfnWs w = ffn_ws(F, backward);
+FfnArgs ffn_args(const moe_ffn* F, const FfnWs& w, void* ws) {
   uint8_t* base = static_cast<uint8_t*>(ws);
-  FfnArgs a{};
+  FfnArgs a = ffn_shape(F);
   a.w_gate = F->bank.w_gate;
   a.w_up = F->bank.w_up;
   a.w_down = F->bank.w_down;
   a.h = base + w.h;
   a.dg = base + w.dg;
   a.du = base + w.du;
-  a.T = F->T;
-  a.d = F->d;
-  a.f = F->f;
-  a.act = F->act;
-  a.f16 = F->bank.fmt == MOE_W_FP16;
   a.status = reinterpret_cast<int32_t*>(base);
+  a.counters = reinterpret_cast<int32_t*>(base + w.g.counters);
+  a.partial = reinterpret_cast<float*>(base + w.g.partial);
+  a.partial_bytes = w.partial_bytes;
   return a;
 }
 
@@ -253,24 +266,23 @@ moe_status moe_ffn_forward(const moe_ffn* F, const void* x, void* y, float* pre,
   if (pre && !is_16bit(F)) return MOE_ERR_UNSUPPORTED;
   if (!x || !aligned(x, 16) || !y || !aligned(y, 16) || !aligned(pre, 16))
     return MOE_ERR_INVALID_ARG;
-  if ((s = ffn_check_ws(F, false, ws, ws_bytes)) != MOE_OK) return s;
+  const FfnWs w = ffn_ws(F, false);
+  if ((s = check_ws(ws, ws_bytes, w.total)) != MOE_OK) return s;
   const size_t xb = (size_t)F->T * F->d * 2, wb = weight_bytes(F), sb = scale_bytes(F);
   const moe_bank& b = F->bank;
-  const Range r[] = {{y, xb}, {pre, (size_t)F->T * F->f * 8}, {ws, ffn_ws(F, false).total}, {x, xb},
+  const Range r[] = {{y, xb}, {pre, (size_t)F->T * F->f * 8}, {ws, w.total}, {x, xb},
                      {b.w_gate, wb}, {b.w_up, wb}, {b.w_down, wb}, {b.s_gate, sb}, {b.s_up, sb},
                      {b.s_down, sb}};
   if (outputs_overlap(r, 3, 10)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  FfnArgs a = ffn_args(F, ws, false);
+  FfnArgs a = ffn_args(F, w, ws);
   if (streams(F, pre)) {
-    uint8_t* base = static_cast<uint8_t*>(ws);
-    const FfnWs w = ffn_ws(F, false);
     for (int i = 0; i < 2; ++i) {
       GemvArgs g = ffn_gemv(F, i);
       g.x = static_cast<const uint16_t*>(i ? a.h : x);
       g.y = i ? y : a.h;
-      g.counters = reinterpret_cast<int32_t*>(base + w.g.counters);
-      g.partial = reinterpret_cast<float*>(base + w.g.partial);
+      g.counters = a.counters;
+      g.partial = a.partial;
       MOE_TRY(launch_gemv_rows(g, st, i == 1));
     }
     return MOE_OK;
@@ -294,15 +306,16 @@ moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void* dy, con
   for (const void* p : {dx, dw_gate, dw_up, dw_down})
     if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_ERR_INVALID_ARG;
-  if ((s = ffn_check_ws(F, true, ws, ws_bytes)) != MOE_OK) return s;
+  const FfnWs w = ffn_ws(F, true);
+  if ((s = check_ws(ws, ws_bytes, w.total)) != MOE_OK) return s;
   const size_t xb = (size_t)F->T * F->d * 2, wb = weight_bytes(F);
   const moe_bank& b = F->bank;
   const Range r[] = {{dx, xb}, {dw_gate, wb}, {dw_up, wb}, {dw_down, wb},
-                     {ws, ffn_ws(F, true).total}, {x, xb}, {dy, xb},
+                     {ws, w.total}, {x, xb}, {dy, xb},
                      {pre, (size_t)F->T * F->f * 8}, {b.w_gate, wb}, {b.w_up, wb}, {b.w_down, wb}};
   if (outputs_overlap(r, 5, 11)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  FfnArgs a = ffn_args(F, ws, true);
+  FfnArgs a = ffn_args(F, w, ws);
   a.x = x;
   a.dy = dy;
   a.pre = const_cast<float*>(pre);
@@ -320,7 +333,7 @@ moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes, in
   moe_status s = ffn_validate(F);
   if (s != MOE_OK) return s;
   if (!code || !site) return MOE_ERR_INVALID_ARG;
-  if ((s = ffn_check_ws(F, false, ws, ws_bytes)) != MOE_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, ffn_ws(F, false).total)) != MOE_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int32_t words[kSiteWord + 1] = {};
   MOE_TRY(cudaMemcpyAsync(words, ws, sizeof(words), cudaMemcpyDeviceToHost, st));

@@ -12,18 +12,27 @@
 // operands; dh never leaves the accumulators, and g and u are kept in fp32: rounding them too
 // would add a second error of the same size to every gradient.
 //
-// One kernel, three epilogues. D[128 x BN] tiles, K in steps of 64 (128 bytes, 128-byte
-// swizzle), both operands by TMA into a ring of stages, tcgen05.mma kind::f16 (M = 128,
-// N = BN) issued by one warp into one of two TMEM accumulators while the epilogue warps empty
-// the other. An operand is read as it lies in memory: with K contiguous (x, dy, h, dg, du and
-// the forward weights) or with K as the slow dimension (the weights of dh and dx, and both
-// operands of the weight gradients), as the MMA's "K-major" or "MN-major" operand; no
-// transposed copies are made. Gate and up rows lie one behind the other in a stage, so a
-// gate/up tile is one MMA whose accumulator holds BN / 2 gate and BN / 2 up columns.
+// One kernel, three epilogues. A pair of CTAs (a cluster of two, tcgen05 cta_group::2) computes
+// D[256 x BN] tiles, K in steps of 64 (128 bytes, 128-byte swizzle): each CTA brings its own 128
+// rows of A and half of B's columns by TMA, the leader's MMA warp issues tcgen05.mma kind::f16
+// (M = 256, N = BN) over both, and each CTA's TMEM receives its 128 rows, in one of two
+// accumulators while the epilogue warps empty the other. Why pairs: an SM takes in about 64
+// bytes a cycle from L2, and a 128 x 256 tile of one CTA needs 96 at the MMA's full rate (967
+// TFLOP/s measured on a 4096 x 2560 x 10240 forward pass), a pair's 256 x 256 tile 64.
+// An operand is read as it lies in memory: with K contiguous (x, dy, h, dg, du and the forward
+// weights) or with K as the slow dimension (the weights of dh and dx, and both operands of the
+// weight gradients), as the MMA's "K-major" or "MN-major" operand; no transposed copies are
+// made. In a gate/up tile one CTA brings gate rows and the other up rows, so the accumulator
+// holds BN / 2 columns of each.
 //
-// Roles (10 warps): warp 0 TMA, warp 1 TMEM and MMA, warps 2..9 epilogue (two warps a TMEM
-// lane quarter, each half of the columns). Every wait is bounded; one that gives up sets the
-// status word and its site, and every role stops.
+// Schedule: static, a tile at a time to each pair, longest products first. Tiles left over by
+// the last full round are split along K over the idle pairs: each part leaves its fp32 sums in
+// the workspace and the epilogue warp that arrives last (a counter per warp) adds the parts in
+// order, so results do not depend on timing and no CTA waits for another.
+//
+// Roles (10 warps): warp 0 TMA, warp 1 TMEM and (leader) MMA, warps 2..9 epilogue (two warps a
+// TMEM lane quarter, each half of the columns). Every wait is bounded; one that gives up sets
+// the status word and its site, and every role stops.
 #include <cstring>
 
 #include "dense.cuh"
@@ -33,10 +42,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 128, kBK = 64;
+constexpr int kBM = 128, kBK = 64;    // rows of one CTA, K values of a step
+constexpr int kPairM = 2 * kBM;
 constexpr int kGemmThreads = 320, kEpiWarps = 8;
-constexpr int kMaxProblems = 4;
-constexpr int kGroupM = 8;           // row tiles walked together, for reuse in L2
+constexpr int kMaxProblems = 4, kMaxPhases = 5;
+constexpr int kMaxPairs = 74;         // CTA pairs of a launch (148 SMs)
+constexpr int kGroupM = 8;            // row tiles walked together, for reuse in L2
 constexpr int kSmemBytes = 227 * 1024;
 
 enum Epi { EPI_STORE = 0, EPI_GATED = 1, EPI_GRAD = 2 };
@@ -51,9 +62,19 @@ struct GemmProblem {
   int tiles_m, tiles_n, first;
 };
 
+// A run of `count` tiles from `first` on, each cut into `splits` K parts, dealt out in turn to
+// the pairs lo .. lo + n - 1. Cut tiles use the counters from `slot` on and the partial sums from
+// `unit` on.
+struct Phase {
+  int first, count, splits, lo, n, slot, unit;
+};
+
 struct GemmArgs {
   GemmProblem p[kMaxProblems];
-  int n, total;
+  Phase ph[kMaxPhases];
+  int n, n_phases;
+  float* partial;     // [unit][rank][BN * 128]
+  int32_t* counters;  // [slot][rank][warp], zero between launches
   // gate/up and gate-gradient epilogues: rows of f elements
   float* pre;
   void* h;
@@ -64,31 +85,60 @@ struct GemmArgs {
 
 template <int BN> struct GemmCfg {
   static constexpr int A_BYTES = kBM * 128;
-  static constexpr int B_BYTES = BN * 128;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int B_BYTES = BN / 2 * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;  // one CTA's share
+  static constexpr int NS = BN == 256 ? 6 : BN == 128 ? 8 : 10;
   static_assert(NS * STAGE + 2048 <= kSmemBytes, "shared memory");
 };
 
-struct Tile {
-  int p, m0, nt;
+// The units of one pair, in order.
+struct Unit {
+  int p, mt, nt;       // problem, tile
+  int k0, k1;          // K steps
+  int splits, part;
+  int slot, unit;      // partial sums: tile and unit
 };
 
-__device__ __forceinline__ Tile tile_at(const GemmArgs& a, int u) {
-  Tile t;
-  t.p = 0;
+struct Walk {
+  int ph, idx, pair;
+  __device__ __forceinline__ explicit Walk(int pair_) : ph(0), idx(-1), pair(pair_) {}
+  // The next unit; false after the last.
+  __device__ __forceinline__ bool next(const GemmArgs& a, Unit* u) {
+    while (ph < a.n_phases) {
+      const Phase& f = a.ph[ph];
+      const int mine = pair - f.lo;
+      if (mine >= 0 && mine < f.n) {
+        idx = idx < 0 ? mine : idx + f.n;
+        if (idx < f.count * f.splits) break;
+      }
+      ++ph;
+      idx = -1;
+    }
+    if (ph >= a.n_phases) return false;
+    const Phase& f = a.ph[ph];
+    const int local = idx / f.splits;
+    const int t = f.first + local;
+    u->splits = f.splits;
+    u->part = idx - local * f.splits;
+    u->slot = f.slot + local;
+    u->unit = f.unit + idx;
+    u->p = 0;
 #pragma unroll
-  for (int i = 1; i < kMaxProblems; ++i)
-    if (i < a.n && u >= a.p[i].first) t.p = i;
-  const GemmProblem& q = a.p[t.p];
-  const int l = u - q.first;
-  const int band = kGroupM * q.tiles_n;
-  const int b = l / band, r = l - b * band;
-  const int rows = min(kGroupM, q.tiles_m - b * kGroupM);
-  t.nt = r / rows;
-  t.m0 = (b * kGroupM + r % rows) * kBM;
-  return t;
-}
+    for (int i = 1; i < kMaxProblems; ++i)
+      if (i < a.n && t >= a.p[i].first) u->p = i;
+    const GemmProblem& q = a.p[u->p];
+    const int l = t - q.first;
+    const int band = kGroupM * q.tiles_n;
+    const int b = l / band, r = l - b * band;
+    const int rows = min(kGroupM, q.tiles_m - b * kGroupM);
+    u->nt = r / rows;
+    u->mt = b * kGroupM + r % rows;
+    const int steps = q.kt[0] + q.kt[1];
+    u->k0 = (int)((long long)steps * u->part / f.splits);
+    u->k1 = (int)((long long)steps * (u->part + 1) / f.splits);
+    return true;
+  }
+};
 
 // Shared-memory descriptor of an operand stored with K as the slow dimension, 128-byte
 // swizzle: blocks of 64 values along M or N (rows of 128 bytes, one a K value) 8192 bytes
@@ -103,13 +153,71 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-// D[tmem] (+)= A B, both operands in shared memory; issued by one elected lane.
-__device__ __forceinline__ void umma_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+// D[tmem] (+)= A B over both CTAs of the pair; issued by one elected lane of the leader.
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Commit of the issued MMAs to the same barrier of both CTAs.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The leader's copy of a shared-memory address.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+// Tile load into this CTA's shared memory, counted on the leader's barrier.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
 
@@ -134,20 +242,23 @@ template <bool F16> __device__ __forceinline__ void store8(void* dst, const floa
 }
 
 template <int BN, int EPI, bool F16, int ACT>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);  // [NS]
+  // 1024-byte alignment by the address inside the CTA's window, so that both CTAs of a pair
+  // have the same layout
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);  // [NS] (leader's used)
   uint64_t* empty = full + C::NS;                                         // [NS]
   uint64_t* acc_full = empty + C::NS;                                     // [2]
-  uint64_t* acc_empty = acc_full + 2;                                     // [2]
+  uint64_t* acc_empty = acc_full + 2;                                     // [2] (leader's used)
   uint64_t* drain = acc_empty + 2;                                        // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -156,15 +267,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kEpiWarps);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 2 * BN);
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -172,103 +285,107 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     set_timeout(a.status, site);
     *abort_flag = 1;
   };
+  Walk walk(pair);
+  Unit u;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------------------------ producer (both CTAs)
     if (lane == 0) {
       int it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < a.total && ok && !*abort_flag; u += gridDim.x) {
-        const Tile t = tile_at(a, u);
-        const GemmProblem& q = a.p[t.p];
-        for (int seg = 0; seg < 2 && ok; ++seg) {
-          const int steps = q.kt[seg];
-          for (int k = 0; k < steps; ++k, ++it) {
-            const int s = it % C::NS, use = it / C::NS;
-            if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            uint8_t* as = smem + s * C::STAGE;
-            uint8_t* bs = as + C::A_BYTES;
-            mbar_arrive_expect_tx(&full[s], C::STAGE);
-            if (q.a_mn) {
+      while (ok && !*abort_flag && walk.next(a, &u)) {
+        const GemmProblem& q = a.p[u.p];
+        const int m0 = u.mt * kPairM + rank * kBM;
+        // this CTA's share of B: columns (rows of the weights) from n0 on; gate/up: all gate
+        // rows in the leader, all up rows in its peer
+        const int n0 = EPI == EPI_GATED ? u.nt * (BN / 2) : u.nt * BN + rank * (BN / 2);
+        for (int k = u.k0; k < u.k1; ++k, ++it) {
+          const int s = it % C::NS, use = it / C::NS;
+          if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const int seg = k >= q.kt[0], kk = (seg ? k - q.kt[0] : k) * kBK;
+          uint8_t* as = smem + s * C::STAGE;
+          uint8_t* bs = as + C::A_BYTES;
+          const uint32_t bar = leader_addr(&full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+          if (q.a_mn) {
 #pragma unroll
-              for (int i = 0; i < kBM / 64; ++i)
-                tma_load_2d(as + i * 8192, &q.a[seg], t.m0 + 64 * i, k * kBK, &full[s]);
-            } else {
-              tma_load_2d(as, &q.a[seg], k * kBK, t.m0, &full[s]);
-            }
-            if constexpr (EPI == EPI_GATED) {
-              tma_load_2d(bs, &q.b[0], k * kBK, t.nt * (BN / 2), &full[s]);
-              tma_load_2d(bs + BN / 2 * 128, &q.b[1], k * kBK, t.nt * (BN / 2), &full[s]);
-            } else if (q.b_mn) {
+            for (int i = 0; i < kBM / 64; ++i)
+              tma_load_pair(as + i * 8192, &q.a[seg], m0 + 64 * i, kk, bar);
+          } else {
+            tma_load_pair(as, &q.a[seg], kk, m0, bar);
+          }
+          if (EPI != EPI_GATED && q.b_mn) {
 #pragma unroll
-              for (int i = 0; i < BN / 64; ++i)
-                tma_load_2d(bs + i * 8192, &q.b[seg], t.nt * BN + 64 * i, k * kBK, &full[s]);
-            } else {
-              tma_load_2d(bs, &q.b[seg], k * kBK, t.nt * BN, &full[s]);
-            }
+            for (int i = 0; i < BN / 128; ++i)
+              tma_load_pair(bs + i * 8192, &q.b[seg], n0 + 64 * i, kk, bar);
+          } else {
+            tma_load_pair(bs, &q.b[EPI == EPI_GATED ? rank : seg], kk, n0, bar);
           }
         }
       }
       if (!ok) fail(50);
-      // every issued stage lands before the CTA may exit
-      for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
-        mbar_wait(&full[j % C::NS], (j / C::NS) & 1);
+      // every issued stage lands before the pair may exit (the leader waits for both shares)
+      if (rank == 0)
+        for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
+          mbar_wait(&full[j % C::NS], (j / C::NS) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    int it = 0, tile = 0;
-    bool aborted = false;
-    for (int u = blockIdx.x; u < a.total && !aborted; u += gridDim.x, ++tile) {
-      const Tile t = tile_at(a, u);
-      const GemmProblem& q = a.p[t.p];
-      const int steps = q.kt[0] + q.kt[1];
-      // D fp32; A and B bf16 (1) or fp16 (0); majors; N; M
-      const uint32_t idesc = (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) |
-                             ((uint32_t)(q.a_mn != 0) << 15) | ((uint32_t)(q.b_mn != 0) << 16) |
-                             ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-      const int b = tile & 1, buse = tile >> 1;
-      if (buse > 0 && !mbar_wait(&acc_empty[b], (buse - 1) & 1)) aborted = true;
-      aborted = __any_sync(0xffffffffu, aborted || *abort_flag);
-      if (aborted) break;
-      tc_fence_after();
-      const uint32_t dacc = tmem + b * BN;
-      const uint64_t astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
-      for (int k = 0; k < steps; ++k, ++it) {
-        const int s = it % C::NS;
-        const bool ok = mbar_wait(&full[s], (it / C::NS) & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          aborted = true;
-          break;
-        }
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (rank == 0) {
+      int it = 0, tile = 0;
+      bool aborted = false;
+      for (; !aborted && walk.next(a, &u); ++tile) {
+        const GemmProblem& q = a.p[u.p];
+        // D fp32; A and B bf16 (1) or fp16 (0); majors; N; M
+        const uint32_t idesc = (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) |
+                               ((uint32_t)(q.a_mn != 0) << 15) | ((uint32_t)(q.b_mn != 0) << 16) |
+                               ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kPairM >> 4) << 24);
+        const int b = tile & 1, buse = tile >> 1;
+        if (buse > 0 && !mbar_wait(&acc_empty[b], (buse - 1) & 1)) aborted = true;
+        aborted = __any_sync(0xffffffffu, aborted || *abort_flag);
+        if (aborted) break;
         tc_fence_after();
-        const uint32_t as = smem_u32(smem + s * C::STAGE), bs = as + C::A_BYTES;
-        const uint64_t ad = q.a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
-        const uint64_t bd = q.b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
+        const uint32_t dacc = tmem + b * BN;
+        const uint64_t astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
+        for (int k = u.k0; k < u.k1; ++k, ++it) {
+          const int s = it % C::NS;
+          const bool ok = mbar_wait(&full[s], (it / C::NS) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t as = smem_u32(smem + s * C::STAGE), bs = as + C::A_BYTES;
+          const uint64_t ad = q.a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
+          const uint64_t bd = q.b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk)
-          umma_f16_warp(dacc, ad + kk * astep, bd + kk * bstep, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-        umma_commit_warp(&empty[s]);
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            umma_f16_pair(dacc, ad + kk * astep, bd + kk * bstep, idesc,
+                          (k > u.k0 || kk > 0) ? 1u : 0u);
+          umma_commit_pair(&empty[s]);
+        }
+        if (aborted) break;
+        umma_commit_pair(&acc_full[b]);
       }
-      if (aborted) break;
-      umma_commit_warp(&acc_full[b]);
+      if (aborted) fail(51);
+      // all issued MMAs complete before TMEM and shared memory are released
+      umma_commit_leader(drain);
+      mbar_wait(drain, 0);
     }
-    if (aborted) fail(51);
-    // all issued MMAs complete before TMEM and shared memory are released
-    umma_commit_warp(drain);
-    mbar_wait(drain, 0);
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     const int quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
     const int half = (warp - 2) >> 2;  // which half of the columns
     constexpr int COLS = EPI == EPI_GATED ? BN / 4 : BN / 2;  // output columns a warp
+    constexpr int ACC = BN / 2;                               // accumulator columns a warp
+    const uint32_t acc_empty_leader[2] = {leader_addr(&acc_empty[0]), leader_addr(&acc_empty[1])};
     int tile = 0;
-    for (int u = blockIdx.x; u < a.total && !*abort_flag; u += gridDim.x, ++tile) {
-      const Tile t = tile_at(a, u);
-      const GemmProblem& q = a.p[t.p];
+    for (; !*abort_flag && walk.next(a, &u); ++tile) {
+      const GemmProblem& q = a.p[u.p];
       const int b = tile & 1;
       if (!mbar_wait(&acc_full[b], (tile >> 1) & 1)) {
         fail(52);
@@ -277,18 +394,86 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       __syncwarp();
       const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * COLS;
-      const int m = t.m0 + quarter * 32 + lane;
-      const int n0 = t.nt * (EPI == EPI_GATED ? BN / 2 : BN) + half * COLS;
+      const int m = u.mt * kPairM + rank * kBM + quarter * 32 + lane;
+      const int n0 = u.nt * (EPI == EPI_GATED ? BN / 2 : BN) + half * COLS;
       const bool row_ok = m < q.M;
+      // Accumulator column i (0..15) of chunk c of this warp: gate/up chunks are 16 gate columns,
+      // then 16 up columns.
+      auto acc_addr = [&](int c) -> uint32_t {
+        if constexpr (EPI == EPI_GATED)
+          return lane_addr + ((c & 16) ? BN / 2 : 0) + (c >> 5) * 16;
+        else
+          return lane_addr + c;
+      };
+      // A part of a split tile: this warp's sums into the workspace, 16 bytes a lane and row of
+      // 512 bytes; the warp that brings the last part goes on with the sum of all.
+      const float4* parts = nullptr;
+      if (u.splits > 1) {
+        const size_t unit_f4 = (size_t)2 * kEpiWarps * (ACC / 4) * 32;
+        const size_t my = ((size_t)rank * kEpiWarps + (warp - 2)) * (ACC / 4) * 32 + lane;
+        float4* base = reinterpret_cast<float4*>(a.partial);
+        float4* dst = base + (size_t)u.unit * unit_f4 + my;
+#pragma unroll 1
+        for (int c = 0; c < ACC; c += 16) {
+          uint32_t r[16];
+          tmem_ld16_async(acc_addr(c), r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            __stcg(dst + (c / 4 + j) * 32,
+                   make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+        }
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          int32_t* cnt = a.counters + ((size_t)u.slot * 2 + rank) * kEpiWarps + (warp - 2);
+          last = atomicAdd(cnt, 1) == u.splits - 1;
+          if (last) *cnt = 0;
+          __threadfence();
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
+        parts = base + (size_t)(u.unit - u.part) * unit_f4 + my;
+        if (!last) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
+          continue;
+        }
+      }
+      // 16 accumulator columns of chunk c; from TMEM without waiting, or the sum of the parts
+      auto load16 = [&](int c, uint32_t (&r)[16]) {
+        if (!parts) {
+          tmem_ld16_async(acc_addr(c), r);
+          return;
+        }
+        const size_t unit_f4 = (size_t)2 * kEpiWarps * (ACC / 4) * 32;
+        float4 v[4] = {};
+        for (int k = 0; k < u.splits; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 w = __ldcg(parts + k * unit_f4 + (c / 4 + j) * 32);
+            v[j].x += w.x, v[j].y += w.y, v[j].z += w.z, v[j].w += w.w;
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          r[4 * j] = __float_as_uint(v[j].x);
+          r[4 * j + 1] = __float_as_uint(v[j].y);
+          r[4 * j + 2] = __float_as_uint(v[j].z);
+          r[4 * j + 3] = __float_as_uint(v[j].w);
+        }
+      };
 #pragma unroll 1
       for (int c = 0; c < COLS; c += 16) {
         const int n = n0 + c;
         const bool ok0 = row_ok && n < q.N, ok1 = row_ok && n + 8 < q.N;  // N is a multiple of 8
         const size_t at = (size_t)m * q.N + n;
         uint32_t r0[16];
-        tmem_ld16_async(lane_addr + c, r0);
         float o[16];
         if constexpr (EPI == EPI_STORE) {
+          load16(c, r0);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(r0[j]);
@@ -297,7 +482,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (ok1) store8<F16>(out + 8, o + 8);
         } else if constexpr (EPI == EPI_GATED) {
           uint32_t r1[16];
-          tmem_ld16_async(lane_addr + BN / 2 + c, r1);
+          load16(2 * c, r0);
+          load16(2 * c + 16, r1);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -327,6 +513,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               u4[j] = pu[j];
             }
           }
+          load16(c, r0);
           tmem_wait_ld();
           float dg[16], du[16];
 #pragma unroll
@@ -354,16 +541,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
     }
   }
 
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    tmem_dealloc_pair(tmem, 2 * BN);
   }
   pdl_trigger();
 }
@@ -371,7 +559,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ------------------------------------------------------------------ host side
 
 template <int BN, int EPI, bool F16, int ACT>
-cudaError_t launch_kernel(const GemmArgs& a, int sms, cudaStream_t st, bool pdl) {
+cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pdl) {
   using C = GemmCfg<BN>;
   auto kern = ffn_gemm_kernel<BN, EPI, F16, ACT>;
   static bool done[kMaxDevices] = {};
@@ -379,7 +567,7 @@ cudaError_t launch_kernel(const GemmArgs& a, int sms, cudaStream_t st, bool pdl)
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(std::min(sms, a.total));
+  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = C::NS * C::STAGE + 2048;
   cfg.stream = st;
@@ -392,14 +580,15 @@ cudaError_t launch_kernel(const GemmArgs& a, int sms, cudaStream_t st, bool pdl)
 }
 
 template <int BN, int EPI>
-cudaError_t launch_types(const GemmArgs& a, bool f16, int act, int sms, cudaStream_t st, bool pdl) {
+cudaError_t launch_types(const GemmArgs& a, bool f16, int act, int pairs, cudaStream_t st,
+                         bool pdl) {
   constexpr int S = MOE_ACT_SILU, G = MOE_ACT_GELU;
   if (EPI == EPI_STORE || act == S)
-    return f16 ? launch_kernel<BN, EPI, true, S>(a, sms, st, pdl)
-               : launch_kernel<BN, EPI, false, S>(a, sms, st, pdl);
+    return f16 ? launch_kernel<BN, EPI, true, S>(a, pairs, st, pdl)
+               : launch_kernel<BN, EPI, false, S>(a, pairs, st, pdl);
   if constexpr (EPI != EPI_STORE)
-    return f16 ? launch_kernel<BN, EPI, true, G>(a, sms, st, pdl)
-               : launch_kernel<BN, EPI, false, G>(a, sms, st, pdl);
+    return f16 ? launch_kernel<BN, EPI, true, G>(a, pairs, st, pdl)
+               : launch_kernel<BN, EPI, false, G>(a, pairs, st, pdl);
   return cudaErrorInvalidValue;
 }
 
@@ -424,43 +613,137 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool f16, int rows_k_major) {
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Tile width: the fewest cycles of the busiest CTA. A 128 x BN x 16 MMA takes BN / 2 cycles,
-// at least the time its operands need from shared memory ((128 + BN) / 4), and a tile about
-// 2000 cycles more to fill the ring and drain the accumulator.
-template <int EPI>
-int pick_bn(const Product* pr, int n, int sms) {
-  int best = 256;
-  double best_cost = -1;
-  for (int bn = 256; bn >= 64; bn /= 2) {
-    long long tiles = 0;
-    double work = 0;
-    for (int i = 0; i < n; ++i) {
-      const int cols = EPI == EPI_GATED ? bn / 2 : bn;
-      const long long t = (long long)((pr[i].M + kBM - 1) / kBM) * ((pr[i].N + cols - 1) / cols);
-      const double step = std::max(bn / 2, (128 + bn) / 4);
-      tiles += t;
-      work += t * ((pr[i].K[0] + pr[i].K[1]) / 16.0 * step + 2000);
+// The schedule of a launch. Tile width and K splits by estimated cycles: a step of 16 K values
+// takes the MMA BN / 2 cycles and a CTA's share of the operands (128 + BN / 2) / 2 (64 bytes a
+// cycle from L2); a tile 1500 more to start and drain; a split tile's part 8 BN cycles to write
+// and each part as much again to read.
+struct GemmPlan {
+  Phase ph[kMaxPhases];
+  int n_phases, bn, units, slots, pairs;
+  int order[kMaxProblems];  // products, longest K first
+  double cost;
+};
+
+double step_cycles(int bn) { return 4.0 * std::max(bn / 2, 64 + bn / 4); }
+
+// Cycles of `r` tiles of `steps` K steps on R idle pairs, split the best way.
+double split_cost(int r, int steps, int R, int bn, int* splits) {
+  double best = -1;
+  for (int s = 1; s <= std::min(std::min(R / r, steps), 16); ++s) {
+    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? (s + 1) * 8.0 * bn + 1000 : 0);
+    if (best < 0 || c < best) {
+      best = c;
+      *splits = s;
     }
-    const double cost = work / tiles * ((tiles + sms - 1) / sms);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = bn;
+  }
+  return best + 1500;
+}
+
+GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
+  GemmPlan g;
+  std::memset(&g, 0, sizeof(g));
+  g.bn = bn;
+  g.pairs = R;
+  int steps[kMaxProblems];
+  long long tiles[kMaxProblems];
+  for (int i = 0; i < n; ++i) {
+    const int cols = gated ? bn / 2 : bn;
+    steps[i] = (pr[i].K[0] + kBK - 1) / kBK + (pr[i].K[1] + kBK - 1) / kBK;
+    tiles[i] = (long long)((pr[i].M + kPairM - 1) / kPairM) * ((pr[i].N + cols - 1) / cols);
+    g.order[i] = i;
+  }
+  std::stable_sort(g.order, g.order + n, [&](int a, int b) { return steps[a] > steps[b]; });
+  // at most two lengths: the input gradient's and the weight gradients'
+  long long count[2] = {0, 0};
+  int len[2] = {steps[g.order[0]], 0};
+  for (int i = 0; i < n; ++i) {
+    const int o = g.order[i];
+    const int c = steps[o] == len[0] ? 0 : 1;
+    if (c) len[1] = steps[o];
+    count[c] += tiles[o];
+  }
+  const auto whole = [&](int c) { return len[c] * step_cycles(bn) + 1500; };
+  int first = 0;
+  const auto add = [&](long long cnt, int splits, int lo, int np) {
+    if (cnt <= 0) return;
+    Phase& f = g.ph[g.n_phases++];
+    f.first = first;
+    f.count = (int)cnt;
+    f.splits = splits;
+    f.lo = lo;
+    f.n = np;
+    f.slot = g.slots;
+    f.unit = g.units;
+    if (splits > 1) {
+      g.slots += (int)cnt;
+      g.units += (int)cnt * splits;
     }
+    first += (int)cnt;
+  };
+  long long full = count[0] / R * R;
+  int e = (int)(count[0] - full);
+  add(full, 1, 0, R);
+  g.cost = full / R * whole(0);
+  if (e && count[1] > 0) {
+    // the leftover long tiles beside as many rounds of short ones on the other pairs, if there
+    // are that many; else split over all pairs
+    const int x = (len[0] + len[1] / 2) / len[1];
+    if ((long long)x * (R - e) <= count[1]) {
+      add(e, 1, 0, e);
+      add((long long)x * (R - e), 1, e, R - e);
+      count[1] -= (long long)x * (R - e);
+      g.cost += whole(0);
+      e = 0;
+    }
+  }
+  if (e) {
+    int s = 1;
+    g.cost += split_cost(e, len[0], R, bn, &s);
+    add(e, s, 0, e * s);
+  }
+  if (count[1] > 0) {
+    full = count[1] / R * R;
+    e = (int)(count[1] - full);
+    add(full, 1, 0, R);
+    g.cost += full / R * whole(1);
+    if (e) {
+      int s = 1;
+      g.cost += split_cost(e, len[1], R, bn, &s);
+      add(e, s, 0, e * s);
+    }
+  }
+  return g;
+}
+
+// 64-column tiles need both operands with K contiguous: a pair's half of 32 columns is no whole
+// 128-byte row of an operand that has K as the slow dimension.
+GemmPlan plan_products(const Product* pr, int n, bool gated, int R) {
+  bool mn = false;
+  for (int i = 0; i < n; ++i) mn = mn || pr[i].b[0].mn;
+  GemmPlan best = plan_width(pr, n, gated, R, 256);
+  for (int bn = 128; bn >= (mn ? 128 : 64); bn /= 2) {
+    const GemmPlan g = plan_width(pr, n, gated, R, bn);
+    if (g.cost < best.cost) best = g;
   }
   return best;
 }
 
+size_t plan_bytes(const GemmPlan& g) { return (size_t)g.units * 2 * kBM * g.bn * sizeof(float); }
+
 template <int EPI>
 cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_t st, bool pdl) {
   const int sms = device_sms();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int bn = pick_bn<EPI>(pr, n, sms);
+  if (sms < 2) return cudaErrorInvalidDevice;
+  const GemmPlan g = plan_products(pr, n, EPI == EPI_GATED, std::min(kMaxPairs, sms / 2));
+  if (plan_bytes(g) > f.partial_bytes) return cudaErrorInvalidValue;
+  const int bn = g.bn;
   GemmArgs a;
   std::memset(&a, 0, sizeof(a));
   a.n = n;
+  int total = 0;
   for (int i = 0; i < n; ++i) {
     GemmProblem& q = a.p[i];
-    const Product& s = pr[i];
+    const Product& s = pr[g.order[i]];
     q.out = s.out;
     q.M = s.M;
     q.N = s.N;
@@ -473,22 +756,29 @@ cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_
     }
     const int n_b = EPI == EPI_GATED ? 2 : segs;
     for (int j = 0; j < n_b; ++j)
-      if (!operand_map(&q.b[j], s.b[j], f.f16, EPI == EPI_GATED ? bn / 2 : bn))
-        return cudaErrorInvalidValue;
+      if (!operand_map(&q.b[j], s.b[j], f.f16, bn / 2)) return cudaErrorInvalidValue;
     const int cols = EPI == EPI_GATED ? bn / 2 : bn;
-    q.tiles_m = (s.M + kBM - 1) / kBM;
+    q.tiles_m = (s.M + kPairM - 1) / kPairM;
     q.tiles_n = (s.N + cols - 1) / cols;
-    q.first = a.total;
-    a.total += q.tiles_m * q.tiles_n;
+    q.first = total;
+    total += q.tiles_m * q.tiles_n;
   }
+  std::memcpy(a.ph, g.ph, sizeof(a.ph));
+  a.n_phases = g.n_phases;
+  a.partial = f.partial;
+  a.counters = f.counters;
   a.pre = f.pre;
   a.h = f.h;
   a.dg = f.dg;
   a.du = f.du;
   a.status = f.status;
-  if (bn == 256) return launch_types<256, EPI>(a, f.f16, f.act, sms, st, pdl);
-  if (bn == 128) return launch_types<128, EPI>(a, f.f16, f.act, sms, st, pdl);
-  return launch_types<64, EPI>(a, f.f16, f.act, sms, st, pdl);
+  int pairs = 0;
+  for (int i = 0; i < g.n_phases; ++i)
+    pairs = std::max(pairs, g.ph[i].lo + std::min(g.ph[i].n, g.ph[i].count * g.ph[i].splits));
+  if (bn == 256) return launch_types<256, EPI>(a, f.f16, f.act, pairs, st, pdl);
+  if (bn == 128) return launch_types<128, EPI>(a, f.f16, f.act, pairs, st, pdl);
+  if constexpr (EPI != EPI_GRAD) return launch_types<64, EPI>(a, f.f16, f.act, pairs, st, pdl);
+  return cudaErrorInvalidValue;
 }
 
 Operand k_major(const void* base, int rows, int cols) {
@@ -498,9 +788,7 @@ Operand mn_major(const void* base, int rows, int cols) {
   return Operand{base, (uint64_t)rows, (uint64_t)cols, true};
 }
 
-}  // namespace
-
-cudaError_t launch_ffn_gate_up(const FfnArgs& f, cudaStream_t st) {
+Product gate_up_product(const FfnArgs& f) {
   Product p{};
   p.a[0] = k_major(f.x, f.T, f.d);
   p.b[0] = k_major(f.w_gate, f.f, f.d);
@@ -508,10 +796,10 @@ cudaError_t launch_ffn_gate_up(const FfnArgs& f, cudaStream_t st) {
   p.K[0] = f.d;
   p.M = f.T;
   p.N = f.f;
-  return run_products<EPI_GATED>(&p, 1, f, st, false);
+  return p;
 }
 
-cudaError_t launch_ffn_down(const FfnArgs& f, cudaStream_t st) {
+Product down_product(const FfnArgs& f) {
   Product p{};
   p.a[0] = k_major(f.h, f.T, f.f);
   p.b[0] = k_major(f.w_down, f.d, f.f);
@@ -519,6 +807,29 @@ cudaError_t launch_ffn_down(const FfnArgs& f, cudaStream_t st) {
   p.M = f.T;
   p.N = f.d;
   p.out = f.y;
+  return p;
+}
+
+}  // namespace
+
+size_t ffn_partial_bytes(const FfnArgs& f, bool backward) {
+  // a launch of the backward pass splits at most its two leftover rounds, whichever outputs
+  // are asked for
+  if (backward) return (size_t)2 * kMaxPairs * kPairM * 256 * sizeof(float);
+  const Product up = gate_up_product(f), down = down_product(f);
+  return std::max(plan_bytes(plan_products(&up, 1, true, kMaxPairs)),
+                  plan_bytes(plan_products(&down, 1, false, kMaxPairs)));
+}
+
+size_t ffn_counters() { return (size_t)2 * kMaxPairs * 2 * kEpiWarps; }
+
+cudaError_t launch_ffn_gate_up(const FfnArgs& f, cudaStream_t st) {
+  const Product p = gate_up_product(f);
+  return run_products<EPI_GATED>(&p, 1, f, st, false);
+}
+
+cudaError_t launch_ffn_down(const FfnArgs& f, cudaStream_t st) {
+  const Product p = down_product(f);
   return run_products<EPI_STORE>(&p, 1, f, st, true);
 }
 
