@@ -19,31 +19,41 @@ cudaError_t allow_smem(const void* kernel, bool* done);
 
 // ------------------------------------------------------------------ activations
 
-// act(g): silu g / (1 + e^-g), or gelu in its tanh form. In fp32; the fast exponential and
-// division are off by a few units in the last place of fp32, far below the 16-bit rounding
-// that follows (e^-g overflowing to infinity gives the limit 0).
-template <int ACT> __device__ __forceinline__ float act_value(float g) {
-  if constexpr (ACT == MOE_ACT_SILU) {
-    return g * __frcp_rn(1.f + __expf(-g));
-  } else {
-    const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    return 0.5f * g * (1.f + tanhf(z));
-  }
+// Both activations are g sigma(k): silu with k = g, gelu in its tanh form with
+// k = 2 sqrt(2 / pi) (g + 0.044715 g^3), since (1 + tanh z) / 2 = sigma(2 z). So one exponential
+// and one reciprocal serve value and slope,
+//   act = g s,  act' = s + g s (1 - s) k',   s = sigma(k),
+// and no difference of near-equal numbers is taken where act is small. In fp32 with the
+// approximate exponential and reciprocal instructions (a few units in the last place, far
+// below the 16-bit rounding that follows; the IEEE reciprocal and tanhf made the gate-gradient
+// epilogue issue 63 instructions a value). e^-k overflowing to infinity gives the limit s = 0.
+__device__ __forceinline__ float sigmoid_approx(float k) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * k));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
 }
 
-// act(g) and act'(g). The polynomial of gelu's derivative takes |g| <= 16: beyond it tanh is
-// exactly +-1 and 1 - tanh^2 is 0, while g^2 could overflow and give 0 * inf.
+constexpr float kGelu1 = 1.5957691216057308f;              // 2 sqrt(2 / pi)
+constexpr float kGelu3 = 1.5957691216057308f * 0.044715f;
+
+template <int ACT> __device__ __forceinline__ float act_value(float g) {
+  if constexpr (ACT == MOE_ACT_SILU) return g * sigmoid_approx(g);
+  else return g * sigmoid_approx(g * fmaf(kGelu3, g * g, kGelu1));
+}
+
+// act(g) and act'(g). Gelu's k' takes |g| <= 16: beyond it s (1 - s) is 0 in fp32, while g^2
+// could overflow and give 0 * inf.
 template <int ACT> __device__ __forceinline__ void act_grad(float g, float* a, float* da) {
   if constexpr (ACT == MOE_ACT_SILU) {
-    const float s = __frcp_rn(1.f + __expf(-g));
+    const float s = sigmoid_approx(g);
     *a = g * s;
-    *da = fmaf(g * s, 1.f - s, s);
+    *da = fmaf(*a, 1.f - s, s);
   } else {
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
+    const float s = sigmoid_approx(g * fmaf(kGelu3, g * g, kGelu1));
     const float c = fminf(fmaxf(g, -16.f), 16.f);
-    *a = 0.5f * g * (1.f + t);
-    *da = 0.5f * (1.f + t) +
-          0.5f * c * (1.f - t * t) * (0.7978845608028654f * (1.f + 0.134145f * c * c));
+    *a = g * s;
+    *da = fmaf(c * s * (1.f - s), fmaf(3.f * kGelu3, c * c, kGelu1), s);
   }
 }
 

@@ -55,7 +55,6 @@ enum Epi { EPI_STORE = 0, EPI_GATED = 1, EPI_GRAD = 2 };
 // One product D[M][N] = sum over up to two K segments of A_s B_s.
 struct GemmProblem {
   CUtensorMap a[2], b[2];  // per segment (EPI_GATED: b[0] gate, b[1] up, both of segment 0)
-  void* out;               // [M][N], 16-bit (EPI_STORE)
   int M, N;                // N: output columns (EPI_GATED: of h)
   int kt[2];               // K steps of each segment
   int a_mn, b_mn;          // operand stored with K as the slow dimension
@@ -73,22 +72,27 @@ struct GemmArgs {
   GemmProblem p[kMaxProblems];
   Phase ph[kMaxPhases];
   int n, n_phases;
+  CUtensorMap o[5];   // outputs by problem (EPI_STORE); h, g, u (EPI_GATED); g, u, h, dg, du
   float* partial;     // [unit][rank][BN * 128]
   int32_t* counters;  // [slot][rank][warp], zero between launches
-  // gate/up and gate-gradient epilogues: rows of f elements
-  float* pre;
-  void* h;
-  void* dg;
-  void* du;
+  int keep;           // EPI_GATED: write g and u
   int32_t* status;
 };
 
-template <int BN> struct GemmCfg {
+template <int BN, int EPI> struct GemmCfg {
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int B_BYTES = BN / 2 * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;  // one CTA's share
-  static constexpr int NS = BN == 256 ? 6 : BN == 128 ? 8 : 10;
-  static_assert(NS * STAGE + 2048 <= kSmemBytes, "shared memory");
+  // output columns of an epilogue warp, and of one of its blocks
+  static constexpr int COLS = EPI == EPI_GATED ? BN / 4 : BN / 2;
+  static constexpr int CH = EPI == EPI_GRAD ? 16 : EPI == EPI_GATED ? (COLS < 32 ? COLS : 32)
+                                                                     : (COLS < 64 ? COLS : 64);
+  // a warp's buffer: 32 rows of a block; the gate gradient's g and u (2048 bytes each) and
+  // three outputs (1024 each)
+  static constexpr int EPI_BYTES = EPI == EPI_GRAD ? 7168 : 4096;
+  static constexpr int NS = (kSmemBytes - 2048 - kEpiWarps * EPI_BYTES) / STAGE;
+  static constexpr int SMEM = NS * STAGE + kEpiWarps * EPI_BYTES + 2048;
+  static_assert(NS >= 4 && STAGE % 1024 == 0 && EPI_BYTES % 1024 == 0 && SMEM <= kSmemBytes, "shared memory");
 };
 
 // The units of one pair, in order.
@@ -207,8 +211,11 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
+// Relaxed: what it hands over are accumulator columns (ordered by the tcgen05 fence before it).
+// A release at cluster scope would wait for the warp's global stores, 14,000 cycles a tile of
+// the gate gradient (measured).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 // Tile load into this CTA's shared memory, counted on the leader's barrier.
@@ -235,25 +242,51 @@ __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 8 consecutive 16-bit results at `dst` (16-byte aligned).
-template <bool F16> __device__ __forceinline__ void store8(void* dst, const float* v) {
-  *static_cast<uint4*>(dst) = make_uint4(pack16x2<F16>(v[0], v[1]), pack16x2<F16>(v[2], v[3]),
-                                         pack16x2<F16>(v[4], v[5]), pack16x2<F16>(v[6], v[7]));
+// Eight fp32 values as 16 bytes of the 16-bit type.
+template <bool F16> __device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack16x2<F16>(v[0], v[1]), pack16x2<F16>(v[2], v[3]), pack16x2<F16>(v[4], v[5]),
+                    pack16x2<F16>(v[6], v[7]));
+}
+
+// 16-byte chunk c of row r in a block of 32 rows x 16 C bytes in shared memory, as TMA's swizzle
+// of that row length lays it out; free of bank conflicts for a lane a row.
+template <int C> __device__ __forceinline__ int block_at(int r, int c) {
+  return (r * C + (c ^ ((r / (8 / C)) & (C - 1)))) * 16;
+}
+// A block to global memory by TMA (which leaves out what lies past the edges), and into it.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last N groups of this thread's stores have read their source / are complete.
+template <int N> __device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <int BN, int EPI, bool F16, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<BN>;
+  using C = GemmCfg<BN, EPI>;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment by the address inside the CTA's window, so that both CTAs of a pair
   // have the same layout
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);  // [NS] (leader's used)
+  uint8_t* epi = smem + C::NS * C::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + kEpiWarps * C::EPI_BYTES);  // [NS] (leader's)
   uint64_t* empty = full + C::NS;                                         // [NS]
   uint64_t* acc_full = empty + C::NS;                                     // [2]
   uint64_t* acc_empty = acc_full + 2;                                     // [2] (leader's used)
-  uint64_t* drain = acc_empty + 2;                                        // [1]
+  uint64_t* pre_full = acc_empty + 2;                                     // [kEpiWarps]
+  uint64_t* drain = pre_full + kEpiWarps;                                 // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -269,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&pre_full[w], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -281,6 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  pdl_trigger();  // the next kernel may set itself up on the SMs that are free
   auto fail = [&](int site) {
     set_timeout(a.status, site);
     *abort_flag = 1;
@@ -380,13 +415,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ------------------------------------------------------------ epilogue (warps 2..9)
     const int quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
     const int half = (warp - 2) >> 2;  // which half of the columns
-    constexpr int COLS = EPI == EPI_GATED ? BN / 4 : BN / 2;  // output columns a warp
-    constexpr int ACC = BN / 2;                               // accumulator columns a warp
+    constexpr int COLS = C::COLS, CH = C::CH;
+    constexpr int ACC = BN / 2;        // accumulator columns a warp
+    uint8_t* buf = epi + (warp - 2) * C::EPI_BYTES;
     const uint32_t acc_empty_leader[2] = {leader_addr(&acc_empty[0]), leader_addr(&acc_empty[1])};
+    const auto first_row = [&](const Unit& v) {
+      return v.mt * kPairM + rank * kBM + quarter * 32;
+    };
+    const auto first_col = [&](const Unit& v) {
+      return v.nt * (EPI == EPI_GATED ? BN / 2 : BN) + half * COLS;
+    };
+    // The gate gradient's g and u of a block into the buffer (lane 0 issues).
+    uint64_t* in_bar = &pre_full[warp - 2];
+    uint32_t in_phase = 0;
+    bool in_flight = false;
+    auto fetch = [&](int m, int n) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(in_bar, 4096);
+        tma_load_2d(buf, &a.o[0], n, m, in_bar);
+        tma_load_2d(buf + 2048, &a.o[1], n, m, in_bar);
+      }
+      in_flight = true;
+    };
     int tile = 0;
-    for (; !*abort_flag && walk.next(a, &u); ++tile) {
+    Unit un;
+    bool more = walk.next(a, &un);
+    if (EPI == EPI_GRAD && more) fetch(first_row(un), first_col(un));
+    for (; !*abort_flag && more; ++tile) {
+      u = un;
+      more = walk.next(a, &un);
       const GemmProblem& q = a.p[u.p];
       const int b = tile & 1;
+      const int m0 = first_row(u), n0 = first_col(u);
       if (!mbar_wait(&acc_full[b], (tile >> 1) & 1)) {
         fail(52);
         break;
@@ -394,9 +454,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       __syncwarp();
       const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * COLS;
-      const int m = u.mt * kPairM + rank * kBM + quarter * 32 + lane;
-      const int n0 = u.nt * (EPI == EPI_GATED ? BN / 2 : BN) + half * COLS;
-      const bool row_ok = m < q.M;
       // Accumulator column i (0..15) of chunk c of this warp: gate/up chunks are 16 gate columns,
       // then 16 up columns.
       auto acc_addr = [&](int c) -> uint32_t {
@@ -436,113 +493,195 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();
         parts = base + (size_t)(u.unit - u.part) * unit_f4 + my;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
         if (!last) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
+          if (EPI == EPI_GRAD && more) {  // the block in the buffer is not this warp's to finish
+            if (!mbar_wait(in_bar, in_phase)) {
+              fail(53);
+              break;
+            }
+            in_phase ^= 1;
+            __syncwarp();
+            fetch(first_row(un), first_col(un));
+          }
           continue;
         }
       }
-      // 16 accumulator columns of chunk c; from TMEM without waiting, or the sum of the parts
-      auto load16 = [&](int c, uint32_t (&r)[16]) {
+      // NC chunks of 16 accumulator columns from chunk column c on: from TMEM, or the sum of the
+      // parts (all loads of a part in flight at once)
+      auto load = [&](int c, auto& r) {
+        constexpr int NC = sizeof(r) / 64;
         if (!parts) {
-          tmem_ld16_async(acc_addr(c), r);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) tmem_ld16_async(acc_addr(c + 16 * i), r[i]);
+          tmem_wait_ld();
           return;
         }
         const size_t unit_f4 = (size_t)2 * kEpiWarps * (ACC / 4) * 32;
-        float4 v[4] = {};
-        for (int k = 0; k < u.splits; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 w = __ldcg(parts + k * unit_f4 + (c / 4 + j) * 32);
-            v[j].x += w.x, v[j].y += w.y, v[j].z += w.z, v[j].w += w.w;
-          }
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r[4 * j] = __float_as_uint(v[j].x);
-          r[4 * j + 1] = __float_as_uint(v[j].y);
-          r[4 * j + 2] = __float_as_uint(v[j].z);
-          r[4 * j + 3] = __float_as_uint(v[j].w);
-        }
-      };
-#pragma unroll 1
-      for (int c = 0; c < COLS; c += 16) {
-        const int n = n0 + c;
-        const bool ok0 = row_ok && n < q.N, ok1 = row_ok && n + 8 < q.N;  // N is a multiple of 8
-        const size_t at = (size_t)m * q.N + n;
-        uint32_t r0[16];
-        float o[16];
-        if constexpr (EPI == EPI_STORE) {
-          load16(c, r0);
-          tmem_wait_ld();
+          for (int j = 0; j < 16; ++j) r[i][j] = 0;  // 0.f
+        for (int k = 0; k < u.splits; ++k) {
+          float4 w[NC][4];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(r0[j]);
-          uint16_t* out = static_cast<uint16_t*>(q.out) + at;
-          if (ok0) store8<F16>(out, o);
-          if (ok1) store8<F16>(out + 8, o + 8);
-        } else if constexpr (EPI == EPI_GATED) {
-          uint32_t r1[16];
-          load16(2 * c, r0);
-          load16(2 * c + 16, r1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o[j] = act_value<ACT>(__uint_as_float(r0[j])) * __uint_as_float(r1[j]);
-          uint16_t* out = static_cast<uint16_t*>(a.h) + at;
-          if (ok0) store8<F16>(out, o);
-          if (ok1) store8<F16>(out + 8, o + 8);
-          if (a.pre) {
-            uint4* pg = reinterpret_cast<uint4*>(a.pre + at);
-            uint4* pu = reinterpret_cast<uint4*>(a.pre + (size_t)q.M * q.N + at);
+          for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (j < 2 ? ok0 : ok1) {
-                pg[j] = make_uint4(r0[4 * j], r0[4 * j + 1], r0[4 * j + 2], r0[4 * j + 3]);
-                pu[j] = make_uint4(r1[4 * j], r1[4 * j + 1], r1[4 * j + 2], r1[4 * j + 3]);
-              }
-          }
-        } else {
-          const float4* pg = reinterpret_cast<const float4*>(a.pre + at);
-          const float4* pu = reinterpret_cast<const float4*>(a.pre + (size_t)q.M * q.N + at);
-          float4 g4[4], u4[4];
+              w[i][j] = __ldcg(parts + k * unit_f4 + (c / 4 + 4 * i + j) * 32);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            g4[j] = u4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < 2 ? ok0 : ok1) {
-              g4[j] = pg[j];
-              u4[j] = pu[j];
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float v[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+              for (int l = 0; l < 4; ++l)
+                r[i][4 * j + l] = __float_as_uint(__uint_as_float(r[i][4 * j + l]) + v[l]);
             }
-          }
-          load16(c, r0);
-          tmem_wait_ld();
-          float dg[16], du[16];
+        }
+      };
+      // the accumulator is free once its last columns are read (a split tile's already is)
+      auto release = [&]() {
+        if (parts) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
+      };
+      // The buffer's previous block has been read; then, after this lane's part is written, the
+      // block may be stored.
+      auto buffer_free = [&]() {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+      };
+      auto buffer_full = [&]() {
+        fence_proxy_async();
+        __syncwarp();
+      };
+      if constexpr (EPI == EPI_STORE) {
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += CH) {
+          uint32_t r[CH / 16][16];
+          load(c, r);
+          if (c + CH == COLS) release();
+          buffer_free();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float dh = __uint_as_float(r0[j]);
-            const float g = reinterpret_cast<const float*>(g4)[j];
-            const float uu = reinterpret_cast<const float*>(u4)[j];
-            float av, dav;
-            act_grad<ACT>(g, &av, &dav);
-            o[j] = av * uu;
-            dg[j] = dh * uu * dav;
-            du[j] = dh * av;
-          }
-          if (ok0) {
-            store8<F16>(static_cast<uint16_t*>(a.h) + at, o);
-            store8<F16>(static_cast<uint16_t*>(a.dg) + at, dg);
-            store8<F16>(static_cast<uint16_t*>(a.du) + at, du);
-          }
-          if (ok1) {
-            store8<F16>(static_cast<uint16_t*>(a.h) + at + 8, o + 8);
-            store8<F16>(static_cast<uint16_t*>(a.dg) + at + 8, dg + 8);
-            store8<F16>(static_cast<uint16_t*>(a.du) + at + 8, du + 8);
+          for (int i = 0; i < CH / 8; ++i)
+            *reinterpret_cast<uint4*>(buf + block_at<CH / 8>(lane, i)) =
+                pack8<F16>(reinterpret_cast<const float*>(&r[i / 2][8 * (i & 1)]));
+          buffer_full();
+          if (lane == 0 && m0 < q.M && n0 + c < q.N) {
+            tma_store_2d(&a.o[u.p], buf, n0 + c, m0);
+            bulk_commit();
           }
         }
+      } else if constexpr (EPI == EPI_GATED) {
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += CH) {
+          uint32_t r[CH / 8][16];  // 16 gate, 16 up columns, and so on
+          load(2 * c, r);
+          if (c + CH == COLS) release();
+          const bool inside = m0 < q.M && n0 + c < q.N;
+          if (a.keep) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              buffer_free();
+#pragma unroll
+              for (int i = 0; i < CH / 4; ++i) {
+                const uint32_t* v = &r[2 * (i / 4) + k][4 * (i & 3)];
+                *reinterpret_cast<uint4*>(buf + block_at<CH / 4>(lane, i)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+              }
+              buffer_full();
+              if (lane == 0 && inside) {
+                tma_store_2d(&a.o[1 + k], buf, n0 + c, m0);
+                bulk_commit();
+              }
+            }
+          }
+          uint4 o4[CH / 8];
+#pragma unroll
+          for (int i = 0; i < CH / 8; ++i) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[j] = act_value<ACT>(__uint_as_float(r[2 * (i / 2)][8 * (i & 1) + j])) *
+                     __uint_as_float(r[2 * (i / 2) + 1][8 * (i & 1) + j]);
+            o4[i] = pack8<F16>(o);
+          }
+          buffer_free();
+#pragma unroll
+          for (int i = 0; i < CH / 8; ++i)
+            *reinterpret_cast<uint4*>(buf + block_at<CH / 8>(lane, i)) = o4[i];
+          buffer_full();
+          if (lane == 0 && inside) {
+            tma_store_2d(&a.o[0], buf, n0 + c, m0);
+            bulk_commit();
+          }
+        }
+      } else {
+        // Blocks of 16 columns. The next block's g and u (of the next unit, at the end) are on
+        // their way while this one is worked on.
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 16) {
+          uint32_t r[1][16];
+          load(c, r);
+          if (c + 16 == COLS) release();
+          ok = __all_sync(0xffffffffu, mbar_wait(in_bar, in_phase));
+          if (!ok) break;
+          in_phase ^= 1;
+          in_flight = false;
+          float4 g4[4], u4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g4[i] = *reinterpret_cast<const float4*>(buf + block_at<4>(lane, i));
+            u4[i] = *reinterpret_cast<const float4*>(buf + 2048 + block_at<4>(lane, i));
+          }
+          __syncwarp();
+          if (c + 16 < COLS) fetch(m0, n0 + c + 16);
+          else if (more) fetch(first_row(un), first_col(un));
+          float o[3][16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float gv[4] = {g4[i].x, g4[i].y, g4[i].z, g4[i].w};
+            const float uv[4] = {u4[i].x, u4[i].y, u4[i].z, u4[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float dh = __uint_as_float(r[0][4 * i + j]);
+              float av, dav;
+              act_grad<ACT>(gv[j], &av, &dav);
+              o[0][4 * i + j] = av * uv[j];
+              o[1][4 * i + j] = dh * uv[j] * dav;
+              o[2][4 * i + j] = dh * av;
+            }
+          }
+          buffer_free();
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(buf + 4096 + k * 1024 + block_at<2>(lane, i)) =
+                  pack8<F16>(&o[k][8 * i]);
+          buffer_full();
+          if (lane == 0 && m0 < q.M && n0 + c < q.N) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              tma_store_2d(&a.o[2 + k], buf + 4096 + k * 1024, n0 + c, m0);
+            bulk_commit();
+          }
+        }
+        if (!ok) {
+          fail(53);
+          break;
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
     }
+    // copies in flight end before the CTA may
+    if (EPI == EPI_GRAD && in_flight) mbar_wait(in_bar, in_phase);
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   // ------------------------------------------------------------ teardown
@@ -553,14 +692,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 2 * BN);
   }
-  pdl_trigger();
 }
 
 // ------------------------------------------------------------------ host side
 
 template <int BN, int EPI, bool F16, int ACT>
 cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pdl) {
-  using C = GemmCfg<BN>;
+  using C = GemmCfg<BN, EPI>;
   auto kern = ffn_gemm_kernel<BN, EPI, F16, ACT>;
   static bool done[kMaxDevices] = {};
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
@@ -569,7 +707,7 @@ cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pd
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = C::NS * C::STAGE + 2048;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -611,6 +749,20 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool f16, int rows_k_major) {
       f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return make_map(m, dt, 2, o.base, o.cols, o.rows, 64, o.mn ? 64 : rows_k_major,
                   CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Blocks of 32 rows x ch columns of a row-major [rows][cols] array; type: 0 bf16, 1 fp16, 2 fp32.
+bool block_map(CUtensorMap* m, const void* base, int rows, int cols, int ch, int type) {
+  const int size = type == 2 ? 4 : 2;
+  const int bytes = ch * size;
+  return make_map(m,
+                  type == 2   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                  : type == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  size, base, cols, rows, ch, 32,
+                  bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 // The schedule of a launch. Tile width and K splits by estimated cycles: a step of 16 K values
@@ -744,7 +896,6 @@ cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_
   for (int i = 0; i < n; ++i) {
     GemmProblem& q = a.p[i];
     const Product& s = pr[g.order[i]];
-    q.out = s.out;
     q.M = s.M;
     q.N = s.N;
     q.a_mn = s.a[0].mn;
@@ -767,10 +918,27 @@ cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_
   a.n_phases = g.n_phases;
   a.partial = f.partial;
   a.counters = f.counters;
-  a.pre = f.pre;
-  a.h = f.h;
-  a.dg = f.dg;
-  a.du = f.du;
+  a.keep = f.pre != nullptr;
+  // outputs (and the gate gradient's inputs) by blocks of 32 rows
+  const int cols = EPI == EPI_GATED ? bn / 4 : bn / 2;
+  const int ch = EPI == EPI_GRAD ? 16 : std::min(cols, EPI == EPI_GATED ? 32 : 64);
+  bool ok = true;
+  if (EPI == EPI_STORE) {
+    for (int i = 0; i < n; ++i) {
+      const Product& s = pr[g.order[i]];
+      ok = ok && block_map(&a.o[i], s.out, s.M, s.N, ch, f.f16 ? 1 : 0);
+    }
+  } else {
+    const size_t rows_f = (size_t)f.T * f.f;
+    const int in = EPI == EPI_GATED ? 1 : 0, first_out = EPI == EPI_GATED ? 0 : 2;
+    if (f.pre)
+      for (int k = 0; k < 2; ++k)
+        ok = ok && block_map(&a.o[in + k], f.pre + k * rows_f, f.T, f.f, ch, 2);
+    void* out[3] = {f.h, f.dg, f.du};
+    for (int k = 0; k < (EPI == EPI_GATED ? 1 : 3); ++k)
+      ok = ok && block_map(&a.o[first_out + k], out[k], f.T, f.f, ch, f.f16 ? 1 : 0);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   a.status = f.status;
   int pairs = 0;
   for (int i = 0; i < g.n_phases; ++i)

@@ -374,8 +374,8 @@ MOE_API moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void*
 
 /* Reads the status word of a block's workspace (synchronises `stream`), writes MOE_OK,
  * MOE_ERR_TIMEOUT or MOE_ERR_DEVICE to *code and the site of the bounded wait that gave up to
- * *site (0: none; 50 stage free, 51 stage landed or accumulator free, 52 accumulator full),
- * and clears both. */
+ * *site (0: none; 50 stage free, 51 stage landed or accumulator free, 52 accumulator full, 53
+ * kept g and u landed), and clears both. */
 MOE_API moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes,
                                          int32_t* code, int32_t* site, moe_stream_t stream);
 
