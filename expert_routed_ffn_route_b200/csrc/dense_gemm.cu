@@ -47,7 +47,7 @@ constexpr int kPairM = 2 * kBM;
 constexpr int kGemmThreads = 320, kEpiWarps = 8;
 constexpr int kMaxProblems = 4, kMaxPhases = 5;
 constexpr int kMaxPairs = 74;         // CTA pairs of a launch (148 SMs)
-constexpr int kGroupM = 8;            // row tiles walked together, for reuse in L2
+constexpr int kGroupM = 16;           // row tiles walked together, for reuse in L2
 constexpr int kSmemBytes = 227 * 1024;
 
 enum Epi { EPI_STORE = 0, EPI_GATED = 1, EPI_GRAD = 2 };
