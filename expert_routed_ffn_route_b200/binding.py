@@ -62,8 +62,9 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_s
            "moe_layer_forward_marked", "moe_device_status", "moe_launches_per_call",
            "moe_layer_forward_static", "moe_static_device_status", "moe_test_inject_hold",
            "moe_nvfp4_pack_scales", "moe_nvfp4_quantize_rows", "moe_device_wait_site",
-           "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec", "moe_ffn_validate",
-           "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_device_status"]
+           "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec",
+           "moe_matvec_device_status", "moe_ffn_validate", "moe_ffn_workspace_size",
+           "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_device_status"]
 
 
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
@@ -105,6 +106,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "moe_matvec_validate": (I32, [MP]),
         "moe_matvec_workspace_size": (SZ, [MP]),
         "moe_matvec": (I32, [MP, P, P, P, SZ, P]),
+        "moe_matvec_device_status": (I32, [MP, P, SZ, ctypes.POINTER(I32), ctypes.POINTER(I32),
+                                           P]),
         "moe_ffn_validate": (I32, [FP]),
         "moe_ffn_workspace_size": (SZ, [FP, I32]),
         "moe_ffn_forward": (I32, [FP, P, P, P, P, SZ, P]),
@@ -378,9 +381,11 @@ def _dtype_code(t) -> int:
 
 def _check_rows(t, name, rows, cols, dtype, device):
     """A [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != (rows, cols):
+    if t.dtype != dtype or t.device != device or t.shape != (rows, cols):
         raise ValueError(f"{name}: expected {dtype} [{rows}, {cols}] on {device}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return
     if t.stride(1) != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     if rows > 1 and t.stride(0) < cols:
@@ -392,13 +397,23 @@ def _check_ws(ws, device):
         raise ValueError(f"the workspace must be contiguous and on {device}")
 
 
+_CURRENT = None  # (current device, its raw stream), bound at the first call
+
+
 def _call(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current; returns its status."""
+    """fn(*args, stream) with `device` current; returns its status. The current stream is asked
+    for as a raw handle: building a torch stream object takes as long as a kernel launch."""
+    global _CURRENT
+    if _CURRENT is None:
+        import torch
+        _CURRENT = (torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+    current_device, raw_stream = _CURRENT
+    index = device.index
+    if index == current_device():
+        return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
     import torch
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
     with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+        return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 def _alloc_zeroed(nbytes: int, device):
@@ -460,20 +475,20 @@ def alloc_matvec_workspace(M: MoeMatrix):
 
 def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     """y = x W^T (+ bias) for the T <= 32 rows of x: [T, K] -> [T, N] (include/moe_b200.h)."""
-    import torch
+    T, N, K, ldy = M.T, M.N, M.K, M.ldy
     dev, (xt, yt) = M.owner.device, M.dtypes
-    _check_rows(x, "x", M.T, M.K, xt, dev)
-    if M.T > 1 and x.stride(0) != M.ldx:
+    _check_rows(x, "x", T, K, xt, dev)
+    if T > 1 and x.stride(0) != M.ldx:
         raise ValueError(f"x: rows are {x.stride(0)} elements apart, the descriptor says {M.ldx}")
     if out is None:
-        out = torch.empty((M.T, M.ldy), dtype=yt, device=dev)
-        if M.ldy != M.N:
-            out = out[:, :M.N]
+        out = x.new_empty((T, ldy), dtype=yt)
+        if ldy != N:
+            out = out[:, :N]
     else:
-        _check_rows(out, "out", M.T, M.N, yt, dev)
-        if M.T > 1 and out.stride(0) != M.ldy:
+        _check_rows(out, "out", T, N, yt, dev)
+        if T > 1 and out.stride(0) != ldy:
             raise ValueError(f"out: rows are {out.stride(0)} elements apart, the descriptor says "
-                             f"{M.ldy}")
+                             f"{ldy}")
     _check_ws(ws, dev)
     _check(_call(dev, stream, load_library().moe_matvec, ctypes.byref(M), x.data_ptr(),
                  out.data_ptr(), ws.data_ptr(), ws.numel()), "moe_matvec")
@@ -539,7 +554,8 @@ def ffn_workspace_size(F: MoeFfn, backward: bool = False) -> int:
 
 
 def alloc_ffn_workspace(F: MoeFfn, backward: bool = False):
-    """A zeroed workspace for ffn_forward, with ``backward`` for ffn_backward too."""
+    """A zeroed workspace for ffn_forward, with ``backward`` for training calls (ffn_forward with
+    pre, and ffn_backward)."""
     return _alloc_zeroed(ffn_workspace_size(F, backward), F.owner.device)
 
 
@@ -551,14 +567,14 @@ def ffn_pre(F: MoeFfn, device=None):
 
 def _check_pre(F: MoeFfn, pre):
     import torch
-    if pre.dtype != torch.float32 or tuple(pre.shape) != (2, F.T, F.f) or \
+    if pre.dtype != torch.float32 or pre.shape != (2, F.T, F.f) or \
             pre.device != F.owner.device or not pre.is_contiguous():
         raise ValueError(f"pre: expected contiguous fp32 [2, {F.T}, {F.f}] on {F.owner.device}")
 
 
 def _check_dense(F: MoeFfn, t, name, rows, cols):
-    if t.dtype != F.owner.dtype or t.device != F.owner.device or \
-            tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+    if t.dtype != F.owner.dtype or t.device != F.owner.device or t.shape != (rows, cols) or \
+            not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {F.owner.dtype} [{rows}, {cols}] on "
                          f"{F.owner.device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
@@ -566,11 +582,10 @@ def _check_dense(F: MoeFfn, t, name, rows, cols):
 def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     """y = Wd (act(Wg x) * (Wu x)) for the rows of x [T, d]; ``pre`` (ffn_pre) keeps what
     ffn_backward needs (include/moe_b200.h)."""
-    import torch
     dev = F.owner.device
     _check_dense(F, x, "x", F.T, F.d)
     if out is None:
-        out = torch.empty_like(x)
+        out = x.new_empty((F.T, F.d))
     else:
         _check_dense(F, out, "out", F.T, F.d)
     if pre is not None:
@@ -585,27 +600,34 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
                  stream=None):
     """(dx, dw_gate, dw_up, dw_down) from dy [T, d], x and the ``pre`` of ffn_forward; what is
     not needed is None and not computed. ``ws``: alloc_ffn_workspace(F, backward=True)."""
-    import torch
     dev = F.owner.device
     _check_dense(F, x, "x", F.T, F.d)
     _check_dense(F, dy, "dy", F.T, F.d)
     _check_pre(F, pre)
     _check_ws(ws, dev)
-    dx = torch.empty_like(x) if need_dx else None
+    dx = x.new_empty((F.T, F.d)) if need_dx else None
     dwg = dwu = dwd = None
     if need_dw:
-        dwg, dwu = (torch.empty((F.f, F.d), dtype=x.dtype, device=dev) for _ in range(2))
-        dwd = torch.empty((F.d, F.f), dtype=x.dtype, device=dev)
+        dwg, dwu = x.new_empty((F.f, F.d)), x.new_empty((F.f, F.d))
+        dwd = x.new_empty((F.d, F.f))
     _check(_call(dev, stream, load_library().moe_ffn_backward, ctypes.byref(F), x.data_ptr(),
                  dy.data_ptr(), pre.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd),
                  ws.data_ptr(), ws.numel()), "moe_ffn_backward")
     return dx, dwg, dwu, dwd
 
 
+def _device_status(fn, D, ws, stream):
+    code, site = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(_call(D.owner.device, stream, fn, ctypes.byref(D), ws.data_ptr(), ws.numel(),
+                 ctypes.byref(code), ctypes.byref(site)), fn.__name__)
+    return code.value, site.value
+
+
 def ffn_device_status(F: MoeFfn, ws, stream=None):
     """(status code, wait site) kept in a block's workspace since the last read (0, 0: none)."""
-    code, site = ctypes.c_int32(0), ctypes.c_int32(0)
-    _check(_call(F.owner.device, stream, load_library().moe_ffn_device_status, ctypes.byref(F),
-                 ws.data_ptr(), ws.numel(), ctypes.byref(code), ctypes.byref(site)),
-           "moe_ffn_device_status")
-    return code.value, site.value
+    return _device_status(load_library().moe_ffn_device_status, F, ws, stream)
+
+
+def matvec_device_status(M: MoeMatrix, ws, stream=None):
+    """(status code, wait site) kept in a matvec workspace since the last read (0, 0: none)."""
+    return _device_status(load_library().moe_matvec_device_status, M, ws, stream)

@@ -91,6 +91,7 @@ struct GemvArgs {
   int gated, act;          // y = act(w[0] x) * (w[1] x)
   float* partial;          // K parts: fp32 sums [tile][part][...]
   int32_t* counters;       // one per row tile, zero between calls
+  int32_t* status;
 };
 
 // Bytes of partial sums and number of counters a call needs (0 when K is not split).
@@ -123,8 +124,9 @@ struct FfnArgs {
   int32_t* counters;   // ffn_counters() of them, zero between calls
 };
 
-// Workspace of the tensor-core kernels: bytes of partial sums, number of counters.
-size_t ffn_partial_bytes(const FfnArgs& a, bool backward);
+// Workspace of the tensor-core kernels, whatever the sizes: bytes of partial sums (a forward
+// launch splits one leftover round of tiles, a backward launch at most two), number of counters.
+size_t ffn_partial_bytes(bool backward);
 size_t ffn_counters();
 
 cudaError_t launch_ffn_gate_up(const FfnArgs& a, cudaStream_t st);          // x -> h (and pre)

@@ -138,15 +138,6 @@ struct FfnWs {
   GemvWs g;
   size_t partial_bytes, h, dg, du, total;
 };
-FfnArgs ffn_shape(const moe_ffn* F) {
-  FfnArgs a{};
-  a.T = F->T;
-  a.d = F->d;
-  a.f = F->f;
-  a.act = F->act;
-  a.f16 = F->bank.fmt == MOE_W_FP16;
-  return a;
-}
 FfnWs ffn_ws(const moe_ffn* F, bool backward) {
   FfnWs w;
   size_t part = 0, cnt = 0;
@@ -157,10 +148,8 @@ FfnWs ffn_ws(const moe_ffn* F, bool backward) {
       part = std::max(part, p);
       cnt = std::max(cnt, c);
     }
-  if (is_16bit(F)) {
-    const FfnArgs a = ffn_shape(F);
-    part = std::max(part, ffn_partial_bytes(a, false));
-    if (backward) part = std::max(part, ffn_partial_bytes(a, true));
+  if (is_16bit(F) && (backward || F->T > kGemvMaxRows)) {
+    part = std::max(part, ffn_partial_bytes(backward));
     cnt = std::max(cnt, ffn_counters());
   }
   w.g = gemv_ws(part, cnt);
@@ -201,7 +190,12 @@ inline size_t scale_bytes(const moe_ffn* F) {
 
 FfnArgs ffn_args(const moe_ffn* F, const FfnWs& w, void* ws) {
   uint8_t* base = static_cast<uint8_t*>(ws);
-  FfnArgs a = ffn_shape(F);
+  FfnArgs a{};
+  a.T = F->T;
+  a.d = F->d;
+  a.f = F->f;
+  a.act = F->act;
+  a.f16 = F->bank.fmt == MOE_W_FP16;
   a.w_gate = F->bank.w_gate;
   a.w_up = F->bank.w_up;
   a.w_down = F->bank.w_down;
@@ -213,6 +207,17 @@ FfnArgs ffn_args(const moe_ffn* F, const FfnWs& w, void* ws) {
   a.partial = reinterpret_cast<float*>(base + w.g.partial);
   a.partial_bytes = w.partial_bytes;
   return a;
+}
+
+// Reads and clears the status and site words at the start of a workspace.
+moe_status read_status(void* ws, int32_t* code, int32_t* site, cudaStream_t st) {
+  int32_t words[kSiteWord + 1] = {};
+  MOE_TRY(cudaMemcpyAsync(words, ws, sizeof(words), cudaMemcpyDeviceToHost, st));
+  MOE_TRY(cudaStreamSynchronize(st));
+  MOE_TRY(cudaMemsetAsync(ws, 0, sizeof(words), st));
+  *code = words[0] == DEV_OK ? MOE_OK : words[0] == DEV_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_ERR_DEVICE;
+  *site = words[kSiteWord];
+  return MOE_OK;
 }
 
 }  // namespace
@@ -244,12 +249,23 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   const GemvWs w = gemv_ws(part, cnt);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(ws);
+  a.status = reinterpret_cast<int32_t*>(base);
   a.x = static_cast<const uint16_t*>(x);
   a.y = y;
   a.counters = reinterpret_cast<int32_t*>(base + w.counters);
   a.partial = reinterpret_cast<float*>(base + w.partial);
   MOE_TRY(launch_gemv_rows(a, reinterpret_cast<cudaStream_t>(stream), false));
   return MOE_OK;
+}
+
+moe_status moe_matvec_device_status(const moe_matrix* M, void* ws, size_t ws_bytes, int32_t* code,
+                                    int32_t* site, moe_stream_t stream) {
+  moe_status s = matvec_validate(M);
+  if (s != MOE_OK) return s;
+  if (!code || !site) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < moe_matvec_workspace_size(M))
+    return MOE_ERR_WORKSPACE;
+  return read_status(ws, code, site, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_ffn_validate(const moe_ffn* F) { return ffn_validate(F); }
@@ -266,7 +282,7 @@ moe_status moe_ffn_forward(const moe_ffn* F, const void* x, void* y, float* pre,
   if (pre && !is_16bit(F)) return MOE_ERR_UNSUPPORTED;
   if (!x || !aligned(x, 16) || !y || !aligned(y, 16) || !aligned(pre, 16))
     return MOE_ERR_INVALID_ARG;
-  const FfnWs w = ffn_ws(F, false);
+  const FfnWs w = ffn_ws(F, pre != nullptr);
   if ((s = check_ws(ws, ws_bytes, w.total)) != MOE_OK) return s;
   const size_t xb = (size_t)F->T * F->d * 2, wb = weight_bytes(F), sb = scale_bytes(F);
   const moe_bank& b = F->bank;
@@ -281,6 +297,7 @@ moe_status moe_ffn_forward(const moe_ffn* F, const void* x, void* y, float* pre,
       GemvArgs g = ffn_gemv(F, i);
       g.x = static_cast<const uint16_t*>(i ? a.h : x);
       g.y = i ? y : a.h;
+      g.status = a.status;
       g.counters = a.counters;
       g.partial = a.partial;
       MOE_TRY(launch_gemv_rows(g, st, i == 1));
@@ -334,14 +351,7 @@ moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes, in
   if (s != MOE_OK) return s;
   if (!code || !site) return MOE_ERR_INVALID_ARG;
   if ((s = check_ws(ws, ws_bytes, ffn_ws(F, false).total)) != MOE_OK) return s;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int32_t words[kSiteWord + 1] = {};
-  MOE_TRY(cudaMemcpyAsync(words, ws, sizeof(words), cudaMemcpyDeviceToHost, st));
-  MOE_TRY(cudaStreamSynchronize(st));
-  MOE_TRY(cudaMemsetAsync(ws, 0, sizeof(words), st));
-  *code = words[0] == DEV_OK ? MOE_OK : words[0] == DEV_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_ERR_DEVICE;
-  *site = words[kSiteWord];
-  return MOE_OK;
+  return read_status(ws, code, site, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

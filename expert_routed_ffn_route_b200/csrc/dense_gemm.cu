@@ -980,13 +980,8 @@ Product down_product(const FfnArgs& f) {
 
 }  // namespace
 
-size_t ffn_partial_bytes(const FfnArgs& f, bool backward) {
-  // a launch of the backward pass splits at most its two leftover rounds, whichever outputs
-  // are asked for
-  if (backward) return (size_t)2 * kMaxPairs * kPairM * 256 * sizeof(float);
-  const Product up = gate_up_product(f), down = down_product(f);
-  return std::max(plan_bytes(plan_products(&up, 1, true, kMaxPairs)),
-                  plan_bytes(plan_products(&down, 1, false, kMaxPairs)));
+size_t ffn_partial_bytes(bool backward) {
+  return (size_t)(backward ? 2 : 1) * kMaxPairs * kPairM * 256 * sizeof(float);
 }
 
 size_t ffn_counters() { return (size_t)2 * kMaxPairs * 2 * kEpiWarps; }

@@ -7,11 +7,13 @@
 // W[n][k] = q[n][k] s[n][k / group].
 //
 // The weights are read once, so a call is bound by streaming them (0.52 bytes a weight for
-// int4 in groups of 128). One CTA of 16 warps per SM. A warp takes 16 weight rows (gated: 8
-// gate rows and the same 8 up rows, so that one lane ends with both sums of an output) and a
-// run of slots of 128 (int4) or 32 (16-bit) K values; each lane copies 16 bytes of two rows a
-// slot into its warp's own ring in shared memory (cp.async, 4 or 8 slots deep, no barrier: a
-// ring is private to its warp) and the copies run ahead across row tiles.
+// int4 in groups of 128). One CTA of 16 warps per SM, a run of row tiles each: 16 weight rows
+// (gated: 8 gate rows and the same 8 up rows, so that one lane ends with both sums of an
+// output). The CTA's work, tiles x slots of 128 bytes of K (256 int4 or 64 16-bit values), is
+// one line cut into 16 equal runs, one a warp, so that no warp waits for another inside the
+// loop; a tile that several warps share is added up in warp order at the end. One lane brings
+// a slot, 16 rows x 128 bytes, into its warp's own ring in shared memory by TMA (whole lines:
+// boxes of 64 bytes reach 5.7 TB/s, of 128 bytes 6.5), 2 to 6 slots ahead of the products.
 //
 // Products: mma.sync m16n8k16, 8 activation rows wide. The int4 codes enter exactly, as the
 // 16-bit values (136 + q) - 136 (bf16) or (1032 + q) - 1032 (fp16): one LOP3 and one packed
@@ -28,81 +30,67 @@
 #include <cstring>
 
 #include "dense.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 16, kWarpsLog2 = 4;
 constexpr int kSmemMax = 227 * 1024;
-constexpr int ring_bytes(int depth) { return kWarps * depth * 1024; }
+constexpr int kSlotBytes = 2048;                 // 16 rows x 128 bytes
+constexpr int kRingSlot = kWarps * kSlotBytes;   // one slot of every warp's ring
+constexpr int kMaxDepth = 6;
+constexpr int kSiteGemvSlot = 60;
 
+// K is counted in units of 64 bytes of a weight row (128 int4 or 32 16-bit values): what 8 (2)
+// MMAs multiply. A slot holds two.
 struct GemvPlan {
-  int slot_k;        // K values a slot
-  int slots;         // slots of a row
+  int unit_k;        // K values a unit
+  int units;         // units of a row
   int parts;         // K parts
-  int part_slots;    // slots a part
+  int part_units;    // units a part (even)
   int tiles;         // row tiles
   int rows;          // output rows a tile
-  int ks;            // warps a tile
-  int groups;        // CTAs a part
-  int run;           // slots a warp
+  int groups;        // CTAs a part, each tiles_q tiles, the first tiles_r one more
+  int tiles_q, tiles_r;
   int tc;            // 8-row column tiles
   int cols;          // activation rows staged (padded to whole column tiles above one)
   int wpr;           // log2 of the warps that stage one row
   int depth;         // ring slots a warp
+  int pdl;           // launched to overlap the kernel before it
   int smem;
 };
 
 GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   GemvPlan p;
-  p.slot_k = a.fmt == 4 ? 128 : 32;
-  p.slots = (a.K + p.slot_k - 1) / p.slot_k;
+  p.unit_k = a.fmt == 4 ? 128 : 32;
+  p.units = (a.K + p.unit_k - 1) / p.unit_k;
   p.tc = a.T <= 8 ? 1 : a.T <= 16 ? 2 : a.T <= 24 ? 3 : 4;
   p.cols = p.tc == 1 ? a.T : 8 * p.tc;
   p.rows = a.gated ? 8 : 16;
   p.tiles = (a.N + p.rows - 1) / p.rows;
-  const int red = kWarps * p.tc * 512;
-  const int slot_bytes = p.slot_k * 2 * p.cols;
-  const int room = kSmemMax - red - 256;
-  // 8 slots deep where one part fits beside it: a call on one row then has 112 KB a SM on the way
-  p.depth = p.tc == 1 && p.slots * slot_bytes <= room - ring_bytes(8) ? 8 : 4;
-  const int fit = std::max(1, (room - ring_bytes(p.depth)) / slot_bytes);
-  p.parts = (p.slots + fit - 1) / fit;
-  p.part_slots = (p.slots + p.parts - 1) / p.parts;
-  p.parts = (p.slots + p.part_slots - 1) / p.part_slots;
-  const int ctas = std::max(1, sms / p.parts);
-  // Warps a tile: the fewest slot steps of the busiest warp, a tile's reduction counted as
-  // two (measured).
-  long long best = -1;
-  p.ks = kWarps;
-  for (int ks = kWarps; ks >= 1; ks /= 2) {
-    const int per = kWarps / ks;                       // tiles a CTA at a time
-    const int g = std::min(ctas, (p.tiles + per - 1) / per);
-    const long long rounds = (p.tiles + (long long)g * per - 1) / ((long long)g * per);
-    const long long cost = rounds * ((p.part_slots + ks - 1) / ks + 2);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.ks = ks;
-    }
-  }
-  const int per = kWarps / p.ks;
-  p.groups = std::min(ctas, (p.tiles + per - 1) / per);
-  p.run = (p.part_slots + p.ks - 1) / p.ks;
+  const int unit_bytes = p.unit_k * 2 * p.cols;
+  const int room = kSmemMax - 2048;                // beside the staged rows: two slots a warp
+  const int fit = std::max(2, (room - 2 * kRingSlot) / unit_bytes & ~1);
+  p.parts = (p.units + fit - 1) / fit;
+  p.part_units = ((p.units + p.parts - 1) / p.parts + 1) & ~1;
+  p.parts = (p.units + p.part_units - 1) / p.part_units;
+  const int xbytes = p.part_units * unit_bytes;
+  p.depth = std::min(kMaxDepth, (room - xbytes) / kRingSlot);
+  p.groups = std::min(std::max(1, sms / p.parts), p.tiles);
+  p.tiles_q = p.tiles / p.groups;
+  p.tiles_r = p.tiles % p.groups;
   p.wpr = 0;
   while ((kWarps >> (p.wpr + 1)) >= a.T) ++p.wpr;
-  p.smem = ring_bytes(p.depth) + red + p.part_slots * slot_bytes + 256;
+  p.pdl = 0;
+  p.smem = p.depth * kRingSlot + xbytes + 2048;
   return p;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+struct GemvMaps {
+  CUtensorMap w[2];  // weight rows in bytes, boxes of 128 bytes x 16 rows (gated: 8)
+};
 
 // c (+)= a b; FIRST starts from zero.
 template <bool F16, bool FIRST = false>
@@ -159,317 +147,371 @@ template <int GROUP> __device__ __forceinline__ void place_of(int w, int* i, int
   }
 }
 
-template <int FMT, int GROUP, bool F16, int TC, bool GATED, int DEPTH>
+template <int FMT, int GROUP, bool F16, int TC, bool GATED>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    gemv_rows_kernel(const GemvArgs a, const GemvPlan p) {
-  constexpr int XI = FMT == 4 ? 4 : 1;             // 16-byte fragment chunks a lane and slot
-  constexpr int NSC = FMT == 4 ? 128 / GROUP : 1;  // scales a row and slot
-  constexpr int SLOT_CHUNKS = FMT == 4 ? 16 : 4;   // chunks of 8 K values a slot
-  constexpr bool EXCHANGE = FMT == 4 && GROUP != 128;  // lanes read words other lanes copied
-  constexpr int RING = ring_bytes(DEPTH);
-  extern __shared__ __align__(1024) uint8_t smem[];
-  float4* red = reinterpret_cast<float4*>(smem + RING);
-  int* last_flag = reinterpret_cast<int*>(smem + RING + kWarps * TC * 512);
-  uint4* xs = reinterpret_cast<uint4*>(smem + RING + kWarps * TC * 512 + 256);
+    gemv_rows_kernel(const __grid_constant__ GemvMaps maps, const GemvArgs a, const GemvPlan p) {
+  constexpr int XI = FMT == 4 ? 4 : 1;             // 16-byte fragment chunks a lane and unit
+  constexpr int NSC = FMT == 4 ? 128 / GROUP : 1;  // scales a row and unit
+  constexpr int UNIT_CHUNKS = FMT == 4 ? 16 : 4;   // chunks of 8 K values a unit
+  constexpr int XB = TC == 1 ? 4 : 10;             // activation chunks a lane has on the way
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.depth * kRingSlot);  // [warp][kMaxDepth]
+  uint4* xs = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(bars) + 1024);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
-  const int ks = warp % p.ks, tg = warp / p.ks, per = kWarps / p.ks;
+  const int t4 = lane & 3;
+  // the tile row of MMA row lane / 4: two rows that one phase of a 16-byte read covers lie four
+  // apart, where the 128-byte swizzle gives them different banks
+  const int g = ((lane >> 2 & 1) << 2) | (lane >> 3);
   const int part = blockIdx.x % p.parts, grp = blockIdx.x / p.parts;
-  const int begin = part * p.part_slots, end = min(p.slots, begin + p.part_slots);
-  const int first = begin + ks * p.run;            // this warp's slots: first .. first + n_my - 1
-  const int n_my = max(0, min(p.run, end - first));
-  const int tile0 = grp * per + tg, tstep = p.groups * per;
-  const size_t row_bytes = FMT == 4 ? (size_t)a.K / 2 : (size_t)a.K * 2;
-  const int chunks = (int)(row_bytes / 16);        // 16-byte chunks a weight row
-  const int n_scales = FMT == 4 ? a.K / GROUP : 0;
+  const int begin = part * p.part_units, n_units = min(p.part_units, p.units - begin);
+  const int n_slots = (n_units + 1) / 2;
+  // tiles of this CTA, and this warp's run of items (tile, slot)
+  const int tb = grp * p.tiles_q + min(grp, p.tiles_r);
+  const int items = (p.tiles_q + (grp < p.tiles_r)) * n_slots;
+  auto run_start = [&](int w) -> int { return (int)((long long)items * w >> kWarpsLog2); };
+  const int lo = run_start(warp), n_my = run_start(warp + 1) - lo;
+  const int tile_off = (int)((unsigned)lo / (unsigned)n_slots);
+  const int tile0 = tb + tile_off, slot0 = lo - tile_off * n_slots;
 
-  // this lane's two rows of a tile (past the end: the last row, never stored)
-  auto row_of = [&](int tile, int half) -> int {
-    const int r = GATED ? tile * 8 + g : tile * 16 + g + 8 * half;
-    return min(r, a.N - 1);
-  };
-  const uint8_t* wbase[2] = {static_cast<const uint8_t*>(a.w[0]),
-                             static_cast<const uint8_t*>(a.w[GATED ? 1 : 0])};
-  const uint16_t* sbase[2] = {a.s[0], a.s[GATED ? 1 : 0]};
-
-  // ---- the ring: the copy cursor runs DEPTH - 1 slots ahead of the products
-  uint8_t* ring = smem + warp * (DEPTH * 1024);
-  // chunk t4 of row g; with groups under 128 a quad exchanges words through the ring, and the
-  // chunk position is rotated by the row so that its 4-byte reads spread over the banks
-  const uint32_t put = smem_u32(ring) +
-                       (EXCHANGE ? g * 64 + (t4 ^ ((g >> 1) & 3)) * 16 : lane * 16);
-  int ct = tile0, cleft = 0, cit = 0;              // copy cursor: tile, slots left in it, count
-  const uint8_t* crow[2];
-  auto copy_tile = [&]() {
-    if (ct < p.tiles && n_my > 0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        crow[h] = wbase[h] + (size_t)row_of(ct, h) * row_bytes + (size_t)first * 64 + t4 * 16;
-      cleft = n_my;
-    }
-  };
-  copy_tile();
+  // ---- the ring (lane 0 issues): `depth` slots ahead of the products
+  uint8_t* ring = smem + warp * (p.depth * kSlotBytes);
+  uint64_t* full = bars + warp * kMaxDepth;
+  int ct = tile0, cs = slot0, cstage = 0, cleft = n_my;  // copy cursor
   auto copy_next = [&]() {
-    if (cleft > 0) {
-      const uint32_t dst = put + (cit % DEPTH) * 1024;
-      // a row may end inside the last slot of its K values (never for groups of 128)
-      bool in = true;
-      if constexpr (FMT != 4 || GROUP != 128) in = (first + n_my - cleft) * 4 + t4 < chunks;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        cp_async16(dst + h * 512, in ? crow[h] : wbase[h], in ? 16u : 0u);
-        crow[h] += 64;
-      }
-      if (--cleft == 0) {
-        ct += tstep;
-        copy_tile();
+    if (cleft <= 0) return;
+    --cleft;
+    if (lane == 0) {
+      uint8_t* dst = ring + cstage * kSlotBytes;
+      const int x = begin * 64 + cs * 128;
+      mbar_arrive_expect_tx(&full[cstage], kSlotBytes);
+      if constexpr (GATED) {
+        tma_load_2d(dst, &maps.w[0], x, ct * 8, &full[cstage]);
+        tma_load_2d(dst + kSlotBytes / 2, &maps.w[1], x, ct * 8, &full[cstage]);
+      } else {
+        tma_load_2d(dst, &maps.w[0], x, ct * 16, &full[cstage]);
       }
     }
-    ++cit;
-    cp_commit();
+    if (++cs == n_slots) {
+      cs = 0;
+      ++ct;
+    }
+    if (++cstage == p.depth) cstage = 0;
   };
-#pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) copy_next();
+  auto start_ring = [&]() {
+    if (lane == 0) {
+      for (int i = 0; i < p.depth; ++i) mbar_init(&full[i], 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    for (int i = 0; i < p.depth; ++i) copy_next();
+  };
 
-  // Scales of four slots at a time, slot 4 b + t4 of batch b in each lane of a quad; the next
-  // batch (of the next tile, at the end) is loaded while one is used.
-  const int batches = (n_my + 3) / 4;
-  int st = tile0, sb = 0;
-  float sc[2][NSC], sn[2][NSC];
+  // ---- scales: a slot ahead, in registers. A quad's lanes hold row half t4 / 2, unit t4 % 2.
+  const int n_scales = FMT == 4 ? a.K / GROUP : 0;
+  int st = tile0, ss = slot0, sleft = n_my;
+  const uint16_t* srow = nullptr;
+  auto scale_tile = [&]() {
+    const int h = t4 >> 1;
+    const int r = min(GATED ? st * 8 + g : st * 16 + g + 8 * h, a.N - 1);
+    srow = (GATED && h ? a.s[1] : a.s[0]) + (size_t)r * n_scales;
+  };
+  uint32_t sn[NSC] = {};
   auto load_scales = [&]() {
-    if (FMT == 4 && st < p.tiles) {
-      const int at = (first + 4 * sb + t4) * NSC;
+    if (FMT != 4 || sleft <= 0) return;
+    --sleft;
+    const int at = (begin + 2 * ss + (t4 & 1)) * NSC;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint16_t* row = sbase[h] + (size_t)row_of(st, h) * n_scales;
-#pragma unroll
-        for (int j = 0; j < NSC; ++j)
-          sn[h][j] = bf16_to_f32(__ldg(row + min(at + j, n_scales - 1)));
-      }
-      if (++sb >= batches) {
-        sb = 0;
-        st += tstep;
-      }
+    for (int j = 0; j < NSC; ++j) sn[j] = __ldg(srow + min(at + j, n_scales - 1));
+    if (++ss == n_slots) {
+      ss = 0;
+      ++st;
+      scale_tile();
     }
   };
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < NSC; ++j) sn[h][j] = 0.f;
-  if (n_my > 0) load_scales();
 
-  // ---- activation rows into shared memory, in fragment order (after the preceding kernel);
-  // 2^wpr warps a row, four chunks a lane on the way at a time
+  // ---- activation rows into shared memory, in fragment order; 2^wpr warps a row, XB chunks a
+  // lane on the way at a time
+  const int c0 = begin * UNIT_CHUNKS, nc = n_units * UNIT_CHUNKS, kc = a.K / 8;
+  const int xstride = 32 << p.wpr;
+  const int xstart = lane + 32 * (warp & ((1 << p.wpr) - 1));
+  const int xwrap = (max(0, nc - xstart) + xstride - 1) & ~(xstride - 1);
+  int xrow = warp >> p.wpr, xc = xstart;
+  uint4 xv[XB];
+  int xrows[XB], xcs[XB];
+  auto fetch_x = [&]() {
+#pragma unroll
+    for (int j = 0; j < XB; ++j) {
+      if (xc >= nc) {                              // on to this warp's next row
+        xc -= xwrap;
+        xrow += kWarps >> p.wpr;
+      }
+      xrows[j] = xrow;
+      xcs[j] = xc;
+      xv[j] = make_uint4(0, 0, 0, 0);
+      if (xrow < a.T && xc < nc && c0 + xc < kc)
+        xv[j] = *(reinterpret_cast<const uint4*>(a.x + (size_t)xrow * a.ldx) + c0 + xc);
+      xc += xstride;
+    }
+  };
+  auto put_x = [&]() {
+#pragma unroll
+    for (int j = 0; j < XB; ++j) {
+      if (xrows[j] >= a.T || xcs[j] >= nc) continue;
+      int fi = 0, ft = xcs[j] % UNIT_CHUNKS;
+      uint4 w = xv[j];
+      if constexpr (FMT == 4) {
+        place_of<GROUP>(xcs[j] % UNIT_CHUNKS, &fi, &ft);
+        // (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
+        w.x = __byte_perm(xv[j].x, xv[j].z, 0x5410);
+        w.y = __byte_perm(xv[j].x, xv[j].z, 0x7632);
+        w.z = __byte_perm(xv[j].y, xv[j].w, 0x5410);
+        w.w = __byte_perm(xv[j].y, xv[j].w, 0x7632);
+      }
+      xs[((xcs[j] / UNIT_CHUNKS * XI + fi) * p.cols + xrows[j]) * 4 + ft] = w;
+    }
+  };
+  // The weights do not depend on the kernel before: with programmatic launch their copies start
+  // first, else the (shorter) rows' do.
+  if (p.pdl) start_ring();
+  if (FMT == 4 && n_my > 0) scale_tile();
+  load_scales();
   pdl_wait();
   pdl_trigger();
-  {
-    const int c0 = begin * SLOT_CHUNKS, nc = (end - begin) * SLOT_CHUNKS, kc = a.K / 8;
-    const int step = 32 << p.wpr;
-    for (int row = warp >> p.wpr; row < a.T; row += kWarps >> p.wpr) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)row * a.ldx) + c0;
-      for (int c = lane + 32 * (warp & ((1 << p.wpr) - 1)); c < nc; c += 4 * step) {
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = make_uint4(0, 0, 0, 0);
-          if (c + j * step < nc && c0 + c + j * step < kc) v[j] = src[c + j * step];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int cj = c + j * step;
-          if (cj >= nc) break;
-          int fi = 0, ft = cj % SLOT_CHUNKS;
-          uint4 w = v[j];
-          if constexpr (FMT == 4) {
-            place_of<GROUP>(cj % SLOT_CHUNKS, &fi, &ft);
-            // (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
-            w.x = __byte_perm(v[j].x, v[j].z, 0x5410);
-            w.y = __byte_perm(v[j].x, v[j].z, 0x7632);
-            w.z = __byte_perm(v[j].y, v[j].w, 0x5410);
-            w.w = __byte_perm(v[j].y, v[j].w, 0x7632);
-          }
-          xs[((cj / SLOT_CHUNKS * XI + fi) * p.cols + row) * 4 + ft] = w;
-        }
-      }
-    }
+  fetch_x();
+  if (!p.pdl) start_ring();
+  put_x();
+  while (xrow < a.T) {
+    fetch_x();
+    put_x();
   }
   __syncthreads();
 
   // this lane's column (beyond the last row of a single column tile: the last one again)
-  const uint8_t* xlane =
-      reinterpret_cast<const uint8_t*>(xs + (TC == 1 ? min(g, a.T - 1) : g) * 4 + t4) +
-      (size_t)(first - begin) * XI * p.cols * 64;
+  const uint8_t* xlane = reinterpret_cast<const uint8_t*>(
+      xs + (TC == 1 ? min(lane >> 2, a.T - 1) : lane >> 2) * 4 + t4);
   const int xstep = p.cols * 64;                   // bytes from one chunk i to the next
-  int it = 0;
-  for (int tile = tile0; tile < p.tiles; tile += tstep) {
-    float acc[TC][4];
-#pragma unroll
-    for (int c = 0; c < TC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[c][j] = 0.f;
+  // 16 bytes of chunk c (0..7, units of 64 bytes side by side) of this lane's row, swizzled
+  const uint32_t chunk_row = (uint32_t)g * 128;
+  auto chunk_at = [&](int c) -> uint32_t { return chunk_row + ((c ^ g) << 4); };
 
-    const uint8_t* xp = xlane;
-    for (int b4 = 0; b4 < n_my; b4 += 4) {
+  // ---- one tile's sums, complete over this CTA's K: to the output, or to the other parts
+  auto finish = [&](int tile, float (&v)[TC][4]) {
+    if (p.parts > 1) {
+      float4* slot0_ = reinterpret_cast<float4*>(a.partial) + (size_t)tile * p.parts * TC * 32 + lane;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int c = 0; c < TC; ++c)
+        __stcg(slot0_ + (part * TC + c) * 32, make_float4(v[c][0], v[c][1], v[c][2], v[c][3]));
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) {
+        last = atomicAdd(a.counters + tile, 1) == p.parts - 1;
+        if (last) a.counters[tile] = 0;
+        __threadfence();
+      }
+      last = __shfl_sync(0xffffffffu, last, 0);
+      if (!last) return;
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NSC; ++j) sc[h][j] = sn[h][j];
-      load_scales();
+      for (int c = 0; c < TC; ++c)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (b4 + u >= n_my) break;
+        for (int j = 0; j < 4; ++j) v[c][j] = 0.f;
+      for (int k = 0; k < p.parts; ++k)
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+          const float4 u = __ldcg(slot0_ + (k * TC + c) * 32);
+          v[c][0] += u.x, v[c][1] += u.y, v[c][2] += u.z, v[c][3] += u.w;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+      const int col = c * 8 + 2 * t4;
+      if constexpr (GATED) {
+        const int n = tile * 8 + g;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (n < a.N && col + j < a.T) {
+            const float act = a.act == MOE_ACT_SILU ? act_value<MOE_ACT_SILU>(v[c][j])
+                                                    : act_value<MOE_ACT_GELU>(v[c][j]);
+            static_cast<uint16_t*>(a.y)[(size_t)(col + j) * a.ldy + n] =
+                round16<F16>(act * v[c][2 + j]);
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = tile * 16 + g + 8 * (j >> 1), cj = col + (j & 1);
+          if (n < a.N && cj < a.T) {
+            const float r = v[c][j] + (a.bias ? __ldg(a.bias + n) : 0.f);
+            const size_t at = (size_t)cj * a.ldy + n;
+            if (a.y32) static_cast<float*>(a.y)[at] = r;
+            else static_cast<uint16_t*>(a.y)[at] = round16<F16>(r);
+          }
+        }
+      }
+    }
+  };
+
+  // ---- the run
+  bool ok = true;                                  // no wait has given up
+  uint32_t phase = 0;
+  int stage = 0, tile = tile0, slot = slot0;
+  bool whole = slot0 == 0;                         // the tile's first slot is in this run
+  float acc[TC][4], head[TC][4];
+#pragma unroll
+  for (int c = 0; c < TC; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[c][j] = head[c][j] = 0.f;
+  const uint8_t* xp = xlane + slot0 * (2 * XI) * xstep;
+  for (int it = 0; it < n_my; ++it) {
+    uint32_t sc[NSC];
+#pragma unroll
+    for (int j = 0; j < NSC; ++j) sc[j] = sn[j] << 16;
+    load_scales();
+    const uint8_t* sp = ring + stage * kSlotBytes;
+    if (ok && !mbar_wait(&full[stage], phase)) {
+      set_timeout(a.status, kSiteGemvSlot);
+      ok = false;
+    }
+    const bool two = 2 * slot + 1 < n_units;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u == 1 && !two) break;
+      uint32_t wa[4], wb[4];
+      if constexpr (FMT == 16 || GROUP == 128) {
+        const uint32_t at = chunk_at(4 * u + t4);
+        const uint4 ua = *reinterpret_cast<const uint4*>(sp + at);
+        const uint4 ub = *reinterpret_cast<const uint4*>(sp + 1024 + at);
+        wa[0] = ua.x, wa[1] = ua.y, wa[2] = ua.z, wa[3] = ua.w;
+        wb[0] = ub.x, wb[1] = ub.y, wb[2] = ub.z, wb[3] = ub.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int w = word_of<GROUP>(i, t4);
+          const uint32_t at = chunk_at(4 * u + (w >> 2)) + (w & 3) * 4;
+          wa[i] = *reinterpret_cast<const uint32_t*>(sp + at);
+          wb[i] = *reinterpret_cast<const uint32_t*>(sp + 1024 + at);
+        }
+      }
+      if (u == 1 || !two) {                        // the slot is read: bring the next one
+        __syncwarp();
+        if (++stage == p.depth) {
+          stage = 0;
+          phase ^= 1;
+        }
         copy_next();
-        cp_wait<DEPTH - 1>();
-        if constexpr (EXCHANGE) __syncwarp();
-        const uint8_t* sp = ring + (it % DEPTH) * 1024;
-        ++it;
-        if constexpr (FMT == 16) {
-          const uint4 wa = *reinterpret_cast<const uint4*>(sp + lane * 16);
-          const uint4 wb = *reinterpret_cast<const uint4*>(sp + 512 + lane * 16);
+      }
+      if constexpr (FMT == 16) {
+#pragma unroll
+        for (int n = 0; n < TC; ++n) {
+          const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512);
+          mma16816<F16>(acc[n], wa[0], wb[0], wa[1], wb[1], x4.x, x4.y);
+          mma16816<F16>(acc[n], wa[2], wb[2], wa[3], wb[3], x4.z, x4.w);
+        }
+        xp += xstep;
+      } else {
+        float c[TC][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          constexpr int kWords = GROUP / 32;  // words a group
+          const uint32_t a0 = codes_pair<F16>(wa[i]), a1 = codes_pair<F16>(wb[i]);
+          const uint32_t a2 = codes_pair<F16>(wa[i] >> 4), a3 = codes_pair<F16>(wb[i] >> 4);
+          const uint32_t a4 = codes_pair<F16>(wa[i] >> 8), a5 = codes_pair<F16>(wb[i] >> 8);
+          const uint32_t a6 = codes_pair<F16>(wa[i] >> 12), a7 = codes_pair<F16>(wb[i] >> 12);
 #pragma unroll
           for (int n = 0; n < TC; ++n) {
             const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512);
-            mma16816<F16>(acc[n], wa.x, wb.x, wa.y, wb.y, x4.x, x4.y);
-            mma16816<F16>(acc[n], wa.z, wb.z, wa.w, wb.w, x4.z, x4.w);
+            if (i % kWords == 0) mma16816<F16, true>(c[n], a0, a1, a2, a3, x4.x, x4.y);
+            else mma16816<F16>(c[n], a0, a1, a2, a3, x4.x, x4.y);
+            mma16816<F16>(c[n], a4, a5, a6, a7, x4.z, x4.w);
           }
           xp += xstep;
-        } else {
-          uint32_t wa[4], wb[4];
-          if constexpr (GROUP == 128) {
-            const uint4 ua = *reinterpret_cast<const uint4*>(sp + lane * 16);
-            const uint4 ub = *reinterpret_cast<const uint4*>(sp + 512 + lane * 16);
-            wa[0] = ua.x, wa[1] = ua.y, wa[2] = ua.z, wa[3] = ua.w;
-            wb[0] = ub.x, wb[1] = ub.y, wb[2] = ub.z, wb[3] = ub.w;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int w = word_of<GROUP>(i, t4);
-              const int at = g * 64 + (((w >> 2) ^ ((g >> 1) & 3)) * 16) + (w & 3) * 4;
-              wa[i] = *reinterpret_cast<const uint32_t*>(sp + at);
-              wb[i] = *reinterpret_cast<const uint32_t*>(sp + 512 + at);
-            }
-          }
-          float c[TC][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            constexpr int kWords = GROUP / 32;  // words a group
-            const uint32_t a0 = codes_pair<F16>(wa[i]), a1 = codes_pair<F16>(wb[i]);
-            const uint32_t a2 = codes_pair<F16>(wa[i] >> 4), a3 = codes_pair<F16>(wb[i] >> 4);
-            const uint32_t a4 = codes_pair<F16>(wa[i] >> 8), a5 = codes_pair<F16>(wb[i] >> 8);
-            const uint32_t a6 = codes_pair<F16>(wa[i] >> 12), a7 = codes_pair<F16>(wb[i] >> 12);
+          if (i % kWords == kWords - 1) {
+            const float s0 = __uint_as_float(__shfl_sync(0xffffffffu, sc[i / kWords], u, 4));
+            const float s1 = __uint_as_float(__shfl_sync(0xffffffffu, sc[i / kWords], 2 + u, 4));
 #pragma unroll
             for (int n = 0; n < TC; ++n) {
-              const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512);
-              if (i % kWords == 0) mma16816<F16, true>(c[n], a0, a1, a2, a3, x4.x, x4.y);
-              else mma16816<F16>(c[n], a0, a1, a2, a3, x4.x, x4.y);
-              mma16816<F16>(c[n], a4, a5, a6, a7, x4.z, x4.w);
-            }
-            xp += xstep;
-            if (i % kWords == kWords - 1) {
-              const float s0 = __shfl_sync(0xffffffffu, sc[0][i / kWords], u, 4);
-              const float s1 = __shfl_sync(0xffffffffu, sc[1][i / kWords], u, 4);
-#pragma unroll
-              for (int n = 0; n < TC; ++n) {
-                acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
-              }
+              acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
+              acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
+              acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
+              acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
             }
           }
-          // every lane has read the slot before the quad's copies reuse it
-          if constexpr (EXCHANGE) __syncwarp();
         }
       }
     }
-
-    // ---- the tile's warps add their sums in warp order, and the outputs are written
-    const int nthr = p.ks * 32, id = ks * 32 + lane, bar = 1 + tg;
-    auto tile_sync = [&]() {
-      if (p.ks > 1) named_bar_sync(bar, nthr);
-      else __syncwarp();
-    };
-    tile_sync();  // the previous tile's sums have been read
-    float4* my = red + (size_t)tg * p.ks * TC * 32;
+    if (++slot == n_slots) {
+      if (whole) {
+        finish(tile, acc);
+      } else {
 #pragma unroll
-    for (int c = 0; c < TC; ++c)
-      my[(ks * TC + c) * 32 + lane] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
-    tile_sync();
-    bool write = true;
-    if (p.parts > 1) {
-      float4* dst = reinterpret_cast<float4*>(a.partial) + ((size_t)tile * p.parts + part) * TC * 32;
-      for (int i = id; i < TC * 32; i += nthr) {
-        float4 v = my[i];
-        for (int k = 1; k < p.ks; ++k) {
-          const float4 u = my[k * TC * 32 + i];
-          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
-        __stcg(dst + i, v);
-      }
-      __threadfence();
-      tile_sync();
-      if (id == 0) {
-        const int old = atomicAdd(a.counters + tile, 1);
-        if (old == p.parts - 1) a.counters[tile] = 0;
-        last_flag[tg] = old == p.parts - 1;
-        __threadfence();
-      }
-      tile_sync();
-      write = last_flag[tg] != 0;
-    }
-    if (write) {
-      for (int i = id; i < TC * 32; i += nthr) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.parts > 1) {
-          const float4* src =
-              reinterpret_cast<const float4*>(a.partial) + (size_t)tile * p.parts * TC * 32 + i;
-          for (int c = 0; c < p.parts; ++c) {
-            const float4 u = __ldcg(src + (size_t)c * TC * 32);
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-          }
-        } else {
-          for (int k = 0; k < p.ks; ++k) {
-            const float4 u = my[k * TC * 32 + i];
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-          }
-        }
-        const int l = i & 31, col = (i >> 5) * 8 + 2 * (l & 3);
-        const float o[4] = {v.x, v.y, v.z, v.w};  // (row, col) (row, col+1) (row+8, ...)
-        if constexpr (GATED) {
-          const int n = tile * 8 + (l >> 2);
+        for (int c = 0; c < TC; ++c)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (n < a.N && col + j < a.T) {
-              const float act = a.act == MOE_ACT_SILU ? act_value<MOE_ACT_SILU>(o[j])
-                                                      : act_value<MOE_ACT_GELU>(o[j]);
-              static_cast<uint16_t*>(a.y)[(size_t)(col + j) * a.ldy + n] =
-                  round16<F16>(act * o[2 + j]);
-            }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = tile * 16 + (l >> 2) + 8 * (j >> 1), c = col + (j & 1);
-            if (n < a.N && c < a.T) {
-              const float r = o[j] + (a.bias ? __ldg(a.bias + n) : 0.f);
-              const size_t at = (size_t)c * a.ldy + n;
-              if (a.y32) static_cast<float*>(a.y)[at] = r;
-              else static_cast<uint16_t*>(a.y)[at] = round16<F16>(r);
-            }
-          }
-        }
+          for (int j = 0; j < 4; ++j) head[c][j] = acc[c][j];
       }
+      slot = 0;
+      ++tile;
+      whole = true;
+      xp = xlane;
+#pragma unroll
+      for (int c = 0; c < TC; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[c][j] = 0.f;
     }
   }
-  cp_wait<0>();
+
+  // ---- tiles that several warps share: each leaves the sums of the tile it did not begin
+  // ("head") in its ring, which nothing is on its way into any more; the warp that began a tile
+  // adds the heads after it to its own, in warp order
+  const bool open = n_my > 0 && slot != 0;         // the last tile goes on in the next warp
+  float4* mine = reinterpret_cast<float4*>(ring) + lane;
+  const bool inside = open && !whole;              // this run lies within one tile
+#pragma unroll
+  for (int c = 0; c < TC; ++c)                     // (zeros without a head)
+    mine[c * 32] = inside ? make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3])
+                          : make_float4(head[c][0], head[c][1], head[c][2], head[c][3]);
+  __syncthreads();
+  if (open && whole) {
+    const int tile_end = (tile - tb + 1) * n_slots;
+    int n = 0;                                     // warps after this one that share the tile
+    while (warp + 1 + n < kWarps && run_start(warp + 1 + n) < tile_end) ++n;
+    const uint8_t* theirs = smem + (warp + 1) * (p.depth * kSlotBytes) + lane * 16;
+    for (int w = 0; w < n; w += 4) {
+      float4 v[4][TC];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+          v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w + i < n)
+            v[i][c] = *reinterpret_cast<const float4*>(theirs + (w + i) * (p.depth * kSlotBytes) +
+                                                       c * 512);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+          acc[c][0] += v[i][c].x, acc[c][1] += v[i][c].y;
+          acc[c][2] += v[i][c].z, acc[c][3] += v[i][c].w;
+        }
+    }
+    finish(tile, acc);
+  }
 }
 
-template <int FMT, int GROUP, bool F16, int TC, bool GATED, int DEPTH>
+template <int FMT, int GROUP, bool F16, int TC, bool GATED>
 cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
-  auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED, DEPTH>;
+  auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED>;
   static bool done[kMaxDevices] = {};
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
   if (err != cudaSuccess) return err;
+  GemvMaps maps;
+  const uint64_t row_bytes = FMT == 4 ? (uint64_t)a.K / 2 : (uint64_t)a.K * 2;
+  for (int i = 0; i < (GATED ? 2 : 1); ++i)
+    if (!make_map(&maps.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w[i], row_bytes, a.N, 128,
+                  GATED ? 8 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(p.groups * p.parts);
@@ -481,18 +523,16 @@ cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, a, p);
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, p);
 }
 
 template <int FMT, int GROUP, bool F16, bool GATED>
 cudaError_t launch_tc(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
   switch (p.tc) {
-    case 1:
-      return p.depth == 8 ? launch_one<FMT, GROUP, F16, 1, GATED, 8>(a, p, st, pdl)
-                          : launch_one<FMT, GROUP, F16, 1, GATED, 4>(a, p, st, pdl);
-    case 2: return launch_one<FMT, GROUP, F16, 2, GATED, 4>(a, p, st, pdl);
-    case 3: return launch_one<FMT, GROUP, F16, 3, GATED, 4>(a, p, st, pdl);
-    default: return launch_one<FMT, GROUP, F16, 4, GATED, 4>(a, p, st, pdl);
+    case 1: return launch_one<FMT, GROUP, F16, 1, GATED>(a, p, st, pdl);
+    case 2: return launch_one<FMT, GROUP, F16, 2, GATED>(a, p, st, pdl);
+    case 3: return launch_one<FMT, GROUP, F16, 3, GATED>(a, p, st, pdl);
+    default: return launch_one<FMT, GROUP, F16, 4, GATED>(a, p, st, pdl);
   }
 }
 
@@ -544,7 +584,8 @@ void gemv_scratch(const GemvArgs& a, size_t* partial_bytes, size_t* n_counters) 
 cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool pdl) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const GemvPlan p = make_gemv_plan(a, sms);
+  GemvPlan p = make_gemv_plan(a, sms);
+  p.pdl = pdl;
   if (p.smem > kSmemMax || p.parts > sms) return cudaErrorInvalidValue;
   return a.f16 ? launch_fmt<true>(a, p, st, pdl) : launch_fmt<false>(a, p, st, pdl);
 }

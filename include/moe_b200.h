@@ -330,6 +330,12 @@ MOE_API size_t moe_matvec_workspace_size(const moe_matrix* M);
 MOE_API moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws,
                               size_t ws_bytes, moe_stream_t stream);
 
+/* Reads the status word of a matvec workspace (synchronises `stream`), writes MOE_OK,
+ * MOE_ERR_TIMEOUT or MOE_ERR_DEVICE to *code and the site of the bounded wait that gave up to
+ * *site (0: none; 60 weight slot landed), and clears both. */
+MOE_API moe_status moe_matvec_device_status(const moe_matrix* M, void* ws, size_t ws_bytes,
+                                            int32_t* code, int32_t* site, moe_stream_t stream);
+
 /* A dense gated feed-forward block, forward and backward:
  *   g = Wg x, u = Wu x, h = act(g) * u, y = Wd h            (rows x [T][d] -> y [T][d])
  *   dh = Wd^T dy, du = dh act(g), dg = dh u act'(g),
@@ -353,9 +359,9 @@ typedef struct {
 /* Host-side validation of a block descriptor (no CUDA call is made). */
 MOE_API moe_status moe_ffn_validate(const moe_ffn* F);
 
-/* Bytes of device workspace of moe_ffn_forward (backward == 0) or of both calls (backward != 0;
- * 0 for an int4 block, which has no backward pass); 0 if F is invalid. Rules as for
- * moe_matvec_workspace_size. */
+/* Bytes of device workspace of moe_ffn_forward without pre (backward == 0), or of it with pre and
+ * of moe_ffn_backward (backward != 0; 0 for an int4 block, which has no backward pass); 0 if F
+ * is invalid. Rules as for moe_matvec_workspace_size. */
 MOE_API size_t moe_ffn_workspace_size(const moe_ffn* F, int32_t backward);
 
 /* y from x. pre: fp32 [2][T][f], receives g, then u, for the backward pass; NULL when none
@@ -375,7 +381,7 @@ MOE_API moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void*
 /* Reads the status word of a block's workspace (synchronises `stream`), writes MOE_OK,
  * MOE_ERR_TIMEOUT or MOE_ERR_DEVICE to *code and the site of the bounded wait that gave up to
  * *site (0: none; 50 stage free, 51 stage landed or accumulator free, 52 accumulator full, 53
- * kept g and u landed), and clears both. */
+ * kept g and u landed, 60 weight slot landed), and clears both. */
 MOE_API moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes,
                                          int32_t* code, int32_t* site, moe_stream_t stream);
 

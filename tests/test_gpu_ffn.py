@@ -69,8 +69,9 @@ def test_forward_matches_64_bits(B, T, d, f, act, dtype):
     B.ffn_forward(desc, x, ws, out=y)
     pbuf, pre = guarded(2 * T, f, F32)
     pre = pre.view(2, T, f)
-    y2 = B.ffn_forward(desc, x, ws, pre=pre)
-    assert B.ffn_device_status(desc, ws) == (0, 0)
+    tws = B.alloc_ffn_workspace(desc, backward=True)
+    y2 = B.ffn_forward(desc, x, tws, pre=pre)
+    assert B.ffn_device_status(desc, ws) == (0, 0) and B.ffn_device_status(desc, tws) == (0, 0)
     ref, bound = ffn_ref(x, *W, act, dtype)["y"]
     for out in (y, y2):
         assert_close(out, ref, bound, dtype, "y")
@@ -256,8 +257,10 @@ def test_refusals(B):
         B.ffn_forward(d4, x, B.alloc_ffn_workspace(d4), pre=B.ffn_pre(d4))
     desc = block.descriptor(4)
     ws = B.alloc_ffn_workspace(desc)
-    with pytest.raises(B.MoeError):  # a forward workspace is too small for the backward pass
-        B.ffn_backward(desc, x, x, B.ffn_pre(desc), ws)
+    for call in (lambda p: B.ffn_backward(desc, x, x, p, ws),
+                 lambda p: B.ffn_forward(desc, x, ws, pre=p)):
+        with pytest.raises(B.MoeError):  # a forward workspace is too small for training calls
+            call(B.ffn_pre(desc))
     for bad in (x.half(), x[:3], x.cpu(), rows(4, 256, BF)[:, ::2]):
         with pytest.raises(ValueError):
             B.ffn_forward(desc, bad, ws)
