@@ -55,7 +55,7 @@ struct GemvPlan {
   int groups;        // CTAs a part, each tiles_q tiles, the first tiles_r one more
   int tiles_q, tiles_r;
   int tc;            // 8-row column tiles
-  int cols;          // activation rows staged (padded to whole column tiles above one)
+  int cols;          // activation rows staged (an even number; whole column tiles above one)
   int wpr;           // log2 of the warps that stage one row
   int depth;         // ring slots a warp
   int pdl;           // launched to overlap the kernel before it
@@ -67,7 +67,7 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   p.unit_k = a.fmt == 4 ? 128 : 32;
   p.units = (a.K + p.unit_k - 1) / p.unit_k;
   p.tc = a.T <= 8 ? 1 : a.T <= 16 ? 2 : a.T <= 24 ? 3 : 4;
-  p.cols = p.tc == 1 ? a.T : 8 * p.tc;
+  p.cols = p.tc == 1 ? (a.T + 1) & ~1 : 8 * p.tc;
   p.rows = a.gated ? 8 : 16;
   p.tiles = (a.N + p.rows - 1) / p.rows;
   const int unit_bytes = p.unit_k * 2 * p.cols;
@@ -269,7 +269,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         w.z = __byte_perm(xv[j].y, xv[j].w, 0x5410);
         w.w = __byte_perm(xv[j].y, xv[j].w, 0x7632);
       }
-      xs[((xcs[j] / UNIT_CHUNKS * XI + fi) * p.cols + xrows[j]) * 4 + ft] = w;
+      // neighbouring rows change places in odd chunk rows, halves of 64 bytes in chunks 2 and 3:
+      // eight neighbouring chunks of a row then lie in different banks
+      const int cr = xcs[j] / UNIT_CHUNKS * XI + fi;
+      xs[(cr * p.cols + (xrows[j] ^ (cr & 1))) * 4 + (ft ^ (fi & 2))] = w;
     }
   };
   // The weights do not depend on the kernel before: with programmatic launch their copies start
@@ -289,59 +292,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   __syncthreads();
 
   // this lane's column (beyond the last row of a single column tile: the last one again)
-  const uint8_t* xlane = reinterpret_cast<const uint8_t*>(
-      xs + (TC == 1 ? min(lane >> 2, a.T - 1) : lane >> 2) * 4 + t4);
-  const int xstep = p.cols * 64;                   // bytes from one chunk i to the next
+  const int col = TC == 1 ? min(lane >> 2, a.T - 1) : lane >> 2;
+  const uint8_t* xlane = reinterpret_cast<const uint8_t*>(xs + col * 4 + t4);
+  const int xflip = (col & 1) ? -64 : 64;          // to the row's place in odd chunk rows
+  const int xswap = (t4 & 2) ? -32 : 32;           // to the swapped place of chunks 2 and 3
+  const int xstep = p.cols * 64;                  // bytes from one chunk i to the next
   // 16 bytes of chunk c (0..7, units of 64 bytes side by side) of this lane's row, swizzled
   const uint32_t chunk_row = (uint32_t)g * 128;
   auto chunk_at = [&](int c) -> uint32_t { return chunk_row + ((c ^ g) << 4); };
 
-  // ---- one tile's sums, complete over this CTA's K: to the output, or to the other parts
-  auto finish = [&](int tile, float (&v)[TC][4]) {
-    if (p.parts > 1) {
-      float4* slot0_ = reinterpret_cast<float4*>(a.partial) + (size_t)tile * p.parts * TC * 32 + lane;
-#pragma unroll
-      for (int c = 0; c < TC; ++c)
-        __stcg(slot0_ + (part * TC + c) * 32, make_float4(v[c][0], v[c][1], v[c][2], v[c][3]));
-      __threadfence();
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) {
-        last = atomicAdd(a.counters + tile, 1) == p.parts - 1;
-        if (last) a.counters[tile] = 0;
-        __threadfence();
-      }
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (!last) return;
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < TC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[c][j] = 0.f;
-      for (int k = 0; k < p.parts; ++k)
-#pragma unroll
-        for (int c = 0; c < TC; ++c) {
-          const float4 u = __ldcg(slot0_ + (k * TC + c) * 32);
-          v[c][0] += u.x, v[c][1] += u.y, v[c][2] += u.z, v[c][3] += u.w;
-        }
-    }
+  // ---- one tile's sums to the output
+  auto write_out = [&](int tile, const float (&v)[TC][4]) {
 #pragma unroll
     for (int c = 0; c < TC; ++c) {
-      const int col = c * 8 + 2 * t4;
+      const int oc = c * 8 + 2 * t4;
       if constexpr (GATED) {
         const int n = tile * 8 + g;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          if (n < a.N && col + j < a.T) {
+          if (n < a.N && oc + j < a.T) {
             const float act = a.act == MOE_ACT_SILU ? act_value<MOE_ACT_SILU>(v[c][j])
                                                     : act_value<MOE_ACT_GELU>(v[c][j]);
-            static_cast<uint16_t*>(a.y)[(size_t)(col + j) * a.ldy + n] =
+            static_cast<uint16_t*>(a.y)[(size_t)(oc + j) * a.ldy + n] =
                 round16<F16>(act * v[c][2 + j]);
           }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int n = tile * 16 + g + 8 * (j >> 1), cj = col + (j & 1);
+          const int n = tile * 16 + g + 8 * (j >> 1), cj = oc + (j & 1);
           if (n < a.N && cj < a.T) {
             const float r = v[c][j] + (a.bias ? __ldg(a.bias + n) : 0.f);
             const size_t at = (size_t)cj * a.ldy + n;
@@ -351,6 +329,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
+  };
+
+  // ---- one tile's sums, complete over this CTA's K: to the output, or beside the other parts'
+  float4* const partial = reinterpret_cast<float4*>(a.partial) + lane;
+  auto finish = [&](int tile, const float (&v)[TC][4]) {
+    if (p.parts == 1) {
+      write_out(tile, v);
+      return;
+    }
+    float4* dst = partial + ((size_t)tile * p.parts + part) * TC * 32;
+#pragma unroll
+    for (int c = 0; c < TC; ++c)
+      __stcg(dst + c * 32, make_float4(v[c][0], v[c][1], v[c][2], v[c][3]));
   };
 
   // ---- the run
@@ -405,7 +396,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if constexpr (FMT == 16) {
 #pragma unroll
         for (int n = 0; n < TC; ++n) {
-          const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512);
+          const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512 + (u ? xflip : 0));
           mma16816<F16>(acc[n], wa[0], wb[0], wa[1], wb[1], x4.x, x4.y);
           mma16816<F16>(acc[n], wa[2], wb[2], wa[3], wb[3], x4.z, x4.w);
         }
@@ -421,7 +412,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const uint32_t a6 = codes_pair<F16>(wa[i] >> 12), a7 = codes_pair<F16>(wb[i] >> 12);
 #pragma unroll
           for (int n = 0; n < TC; ++n) {
-            const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512);
+            const uint4 x4 = *reinterpret_cast<const uint4*>(
+                xp + n * 512 + ((i & 1) ? xflip : 0) + ((i & 2) ? xswap : 0));
             if (i % kWords == 0) mma16816<F16, true>(c[n], a0, a1, a2, a3, x4.x, x4.y);
             else mma16816<F16>(c[n], a0, a1, a2, a3, x4.x, x4.y);
             mma16816<F16>(c[n], a4, a5, a6, a7, x4.z, x4.w);
@@ -474,8 +466,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   __syncthreads();
   if (open && whole) {
     const int tile_end = (tile - tb + 1) * n_slots;
-    int n = 0;                                     // warps after this one that share the tile
-    while (warp + 1 + n < kWarps && run_start(warp + 1 + n) < tile_end) ++n;
+    // warps after this one that share the tile: run_start(w) < tile_end
+    const int n = min(kWarps, (int)(((unsigned)tile_end * kWarps + items - 1) / (unsigned)items)) -
+                  warp - 1;
     const uint8_t* theirs = smem + (warp + 1) * (p.depth * kSlotBytes) + lane * 16;
     for (int w = 0; w < n; w += 4) {
       float4 v[4][TC];
@@ -497,6 +490,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
     }
     finish(tile, acc);
+  }
+
+  // ---- K parts: this warp's tiles are a run too. One fence, one count a tile, then the sums of
+  // the tiles whose last part this was.
+  if (p.parts > 1) {
+    const int from = tile0 + (slot0 != 0), to = tile + (open && whole);
+    __threadfence();
+    __syncwarp();
+    for (int t0 = from; t0 < to; t0 += 32) {
+      bool last = false;
+      if (t0 + lane < to) {
+        last = atomicAdd(a.counters + t0 + lane, 1) == p.parts - 1;
+        if (last) a.counters[t0 + lane] = 0;
+      }
+      uint32_t mask = __ballot_sync(0xffffffffu, last);
+      if (mask) __threadfence();
+      while (mask) {
+        const int t = t0 + __ffs(mask) - 1;
+        mask &= mask - 1;
+        const float4* src = partial + (size_t)t * p.parts * TC * 32;
+#pragma unroll
+        for (int c = 0; c < TC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[c][j] = 0.f;
+        for (int k = 0; k < p.parts; ++k)
+#pragma unroll
+          for (int c = 0; c < TC; ++c) {
+            const float4 v = __ldcg(src + (k * TC + c) * 32);
+            acc[c][0] += v.x, acc[c][1] += v.y, acc[c][2] += v.z, acc[c][3] += v.w;
+          }
+        write_out(t, acc);
+      }
+    }
   }
 }
 
