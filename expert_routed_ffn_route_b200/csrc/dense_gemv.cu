@@ -238,31 +238,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int xstart = lane + 32 * (warp & ((1 << p.wpr) - 1));
   const int xwrap = (max(0, nc - xstart) + xstride - 1) & ~(xstride - 1);
   int xrow = warp >> p.wpr, xc = xstart;
+  const uint4* xsrc = reinterpret_cast<const uint4*>(a.x + (size_t)xrow * a.ldx) + c0;
+  const size_t xrow_step = (size_t)(kWarps >> p.wpr) * (a.ldx / 8);
   uint4 xv[XB];
-  int xrows[XB], xcs[XB];
+  int xat[XB];                                     // row in the upper half, chunk in the lower
   auto fetch_x = [&]() {
 #pragma unroll
     for (int j = 0; j < XB; ++j) {
       if (xc >= nc) {                              // on to this warp's next row
         xc -= xwrap;
         xrow += kWarps >> p.wpr;
+        xsrc += xrow_step;
       }
-      xrows[j] = xrow;
-      xcs[j] = xc;
+      const bool in = xrow < a.T && xc < nc;
+      xat[j] = in ? xrow << 16 | xc : -1;
       xv[j] = make_uint4(0, 0, 0, 0);
-      if (xrow < a.T && xc < nc && c0 + xc < kc)
-        xv[j] = *(reinterpret_cast<const uint4*>(a.x + (size_t)xrow * a.ldx) + c0 + xc);
+      if (in && c0 + xc < kc) xv[j] = xsrc[xc];
       xc += xstride;
     }
   };
   auto put_x = [&]() {
 #pragma unroll
     for (int j = 0; j < XB; ++j) {
-      if (xrows[j] >= a.T || xcs[j] >= nc) continue;
-      int fi = 0, ft = xcs[j] % UNIT_CHUNKS;
+      if (xat[j] < 0) continue;
+      const int row = xat[j] >> 16, c = xat[j] & 0xffff;
+      int fi = 0, ft = c % UNIT_CHUNKS;
       uint4 w = xv[j];
       if constexpr (FMT == 4) {
-        place_of<GROUP>(xcs[j] % UNIT_CHUNKS, &fi, &ft);
+        place_of<GROUP>(c % UNIT_CHUNKS, &fi, &ft);
         // (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
         w.x = __byte_perm(xv[j].x, xv[j].z, 0x5410);
         w.y = __byte_perm(xv[j].x, xv[j].z, 0x7632);
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
       // neighbouring rows change places in odd chunk rows, halves of 64 bytes in chunks 2 and 3:
       // eight neighbouring chunks of a row then lie in different banks
-      const int cr = xcs[j] / UNIT_CHUNKS * XI + fi;
-      xs[(cr * p.cols + (xrows[j] ^ (cr & 1))) * 4 + (ft ^ (fi & 2))] = w;
+      const int cr = c / UNIT_CHUNKS * XI + fi;
+      xs[(cr * p.cols + (row ^ (cr & 1))) * 4 + (ft ^ (fi & 2))] = w;
     }
   };
   // The weights do not depend on the kernel before: with programmatic launch their copies start
@@ -302,32 +305,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   auto chunk_at = [&](int c) -> uint32_t { return chunk_row + ((c ^ g) << 4); };
 
   // ---- one tile's sums to the output
+  const int esize = a.y32 ? 4 : 2;
   auto write_out = [&](int tile, const float (&v)[TC][4]) {
+    const int n = GATED ? tile * 8 + g : tile * 16 + g;
+    const size_t col_bytes = (size_t)a.ldy * esize;
+    uint8_t* at = static_cast<uint8_t*>(a.y) + (size_t)n * esize + (2 * t4) * col_bytes;
+    const bool ok0 = n < a.N, ok1 = !GATED && n + 8 < a.N;
+    float b0 = 0.f, b1 = 0.f;
+    if (!GATED && a.bias) {
+      if (ok0) b0 = __ldg(a.bias + n);
+      if (ok1) b1 = __ldg(a.bias + n + 8);
+    }
 #pragma unroll
     for (int c = 0; c < TC; ++c) {
-      const int oc = c * 8 + 2 * t4;
-      if constexpr (GATED) {
-        const int n = tile * 8 + g;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (n < a.N && oc + j < a.T) {
+      for (int j = 0; j < 2; ++j)
+        if (c * 8 + 2 * t4 + j < a.T) {
+          uint8_t* to = at + j * col_bytes;
+          if constexpr (GATED) {
             const float act = a.act == MOE_ACT_SILU ? act_value<MOE_ACT_SILU>(v[c][j])
                                                     : act_value<MOE_ACT_GELU>(v[c][j]);
-            static_cast<uint16_t*>(a.y)[(size_t)(oc + j) * a.ldy + n] =
-                round16<F16>(act * v[c][2 + j]);
-          }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = tile * 16 + g + 8 * (j >> 1), cj = oc + (j & 1);
-          if (n < a.N && cj < a.T) {
-            const float r = v[c][j] + (a.bias ? __ldg(a.bias + n) : 0.f);
-            const size_t at = (size_t)cj * a.ldy + n;
-            if (a.y32) static_cast<float*>(a.y)[at] = r;
-            else static_cast<uint16_t*>(a.y)[at] = round16<F16>(r);
+            if (ok0) *reinterpret_cast<uint16_t*>(to) = round16<F16>(act * v[c][2 + j]);
+          } else if (a.y32) {
+            if (ok0) *reinterpret_cast<float*>(to) = v[c][j] + b0;
+            if (ok1) *reinterpret_cast<float*>(to + 32) = v[c][2 + j] + b1;
+          } else {
+            if (ok0) *reinterpret_cast<uint16_t*>(to) = round16<F16>(v[c][j] + b0);
+            if (ok1) *reinterpret_cast<uint16_t*>(to + 16) = round16<F16>(v[c][2 + j] + b1);
           }
         }
-      }
+      at += 8 * col_bytes;
     }
   };
 
