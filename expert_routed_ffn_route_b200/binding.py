@@ -379,40 +379,40 @@ def _dtype_code(t) -> int:
         raise ValueError(f"element type {t} is not supported") from None
 
 
-def _check_rows(t, name, rows, cols, dtype, device):
-    """A [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected {dtype} [{rows}, {cols}] on {device}, got {t.dtype} "
+def _check_rows(t, name, shape, dtype, index, stride=None):
+    """A 2-D tensor of `shape` on CUDA device `index` with contiguous rows, `stride` elements
+    apart where there is more than one (dense without a stride)."""
+    if t.dtype != dtype or t.get_device() != index or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on cuda:{index}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
-    if t.is_contiguous():
-        return
-    if t.stride(1) != 1 and cols > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name}: rows must not overlap")
+    rows, cols = shape
+    want = cols if stride is None else stride
+    if (rows > 1 and t.stride(0) != want) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected rows of contiguous elements, {want} apart, got strides "
+                         f"{list(t.stride())}")
 
 
-def _check_ws(ws, device):
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous and on {device}")
+def _check_ws(ws, index):
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on cuda:{index}")
 
 
 _CURRENT = None  # (current device, its raw stream), bound at the first call
 
 
-def _call(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current; returns its status. The current stream is asked
-    for as a raw handle: building a torch stream object takes as long as a kernel launch."""
+def _call(index, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current; returns its status. The current stream
+    is asked for as a raw handle: building a torch stream object takes as long as a kernel
+    launch."""
     global _CURRENT
     if _CURRENT is None:
         import torch
-        _CURRENT = (torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+        _CURRENT = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     current_device, raw_stream = _CURRENT
-    index = device.index
     if index == current_device():
         return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
     import torch
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
 
 
@@ -438,10 +438,8 @@ class QuantMatrix:
         N, dev = codes.shape[0], codes.device
         if codes.dtype not in (torch.int32, torch.uint32):
             raise ValueError("codes must hold 32-bit words")
-        _check_rows(codes, "codes", N, K // 8, codes.dtype, dev)
-        _check_rows(scales, "scales", N, K // group, torch.bfloat16, dev)
-        if not codes.is_contiguous() or not scales.is_contiguous():
-            raise ValueError("codes and scales must be contiguous")
+        _check_rows(codes, "codes", (N, K // 8), codes.dtype, dev.index)
+        _check_rows(scales, "scales", (N, K // group), torch.bfloat16, dev.index)
         if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or
                                  bias.device != dev or not bias.is_contiguous()):
             raise ValueError(f"bias: expected contiguous fp32 [{N}] on {dev}")
@@ -460,8 +458,11 @@ class QuantMatrix:
                       self.K if ldx is None else ldx, self.N if ldy is None else ldy,
                       self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.bias))
         M.owner = self
-        M.dtypes = (x_dtype, y_dtype)
-        _check(load_library().moe_matvec_validate(ctypes.byref(M)), "moe_matvec_validate")
+        lib = load_library()
+        _check(lib.moe_matvec_validate(ctypes.byref(M)), "moe_matvec_validate")
+        # what each call needs, at hand: a call costs the host little more than its launch
+        M.call = ((T, self.K), (T, self.N), M.ldx, M.ldy, x_dtype, y_dtype, self.device.index,
+                  ctypes.byref(M), lib.moe_matvec)
         return M
 
 
@@ -475,23 +476,18 @@ def alloc_matvec_workspace(M: MoeMatrix):
 
 def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     """y = x W^T (+ bias) for the T <= 32 rows of x: [T, K] -> [T, N] (include/moe_b200.h)."""
-    T, N, K, ldy = M.T, M.N, M.K, M.ldy
-    dev, (xt, yt) = M.owner.device, M.dtypes
-    _check_rows(x, "x", T, K, xt, dev)
-    if T > 1 and x.stride(0) != M.ldx:
-        raise ValueError(f"x: rows are {x.stride(0)} elements apart, the descriptor says {M.ldx}")
+    x_shape, y_shape, ldx, ldy, xt, yt, index, ref, fn = M.call
+    _check_rows(x, "x", x_shape, xt, index, ldx)
     if out is None:
-        out = x.new_empty((T, ldy), dtype=yt)
-        if ldy != N:
-            out = out[:, :N]
+        out = x.new_empty((y_shape[0], ldy), dtype=yt)
+        if ldy != y_shape[1]:
+            out = out[:, :y_shape[1]]
     else:
-        _check_rows(out, "out", T, N, yt, dev)
-        if T > 1 and out.stride(0) != ldy:
-            raise ValueError(f"out: rows are {out.stride(0)} elements apart, the descriptor says "
-                             f"{ldy}")
-    _check_ws(ws, dev)
-    _check(_call(dev, stream, load_library().moe_matvec, ctypes.byref(M), x.data_ptr(),
-                 out.data_ptr(), ws.data_ptr(), ws.numel()), "moe_matvec")
+        _check_rows(out, "out", y_shape, yt, index, ldy)
+    _check_ws(ws, index)
+    status = _call(index, stream, fn, ref, x.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+    if status:
+        _check(status, "moe_matvec")
     return out
 
 
@@ -525,24 +521,23 @@ class DeviceFfn:
             int4 = fmt == "int4"
             want = w.dtype if int4 and w.dtype in (torch.int32, torch.uint32) else \
                 torch.int32 if int4 else self.dtype
-            _check_rows(w, "w_" + m, N, K // 8 if int4 else K, want, self.device)
-            mats = [("w_" + m, w)]
+            _check_rows(w, "w_" + m, (N, K // 8 if int4 else K), want, self.device.index)
+            self.bank["w_" + m] = w
             if int4:
                 s = bank["s_" + m]
                 s = s[0] if s.dim() == 3 and s.shape[0] == 1 else s
-                _check_rows(s, "s_" + m, N, K // 128, torch.bfloat16, self.device)
-                mats.append(("s_" + m, s))
-            for name, t in mats:
-                if not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous")
-                self.bank[name] = t
+                _check_rows(s, "s_" + m, (N, K // 128), torch.bfloat16, self.device.index)
+                self.bank["s_" + m] = s
 
     def descriptor(self, T: int) -> MoeFfn:
         """The descriptor of calls on T rows. It holds pointers into this object's tensors,
         which must outlive it."""
         F = MoeFfn(T, self.d, self.f, ACT_CODE[self.act], bank_struct(self.bank))
         F.owner = self
-        _check(load_library().moe_ffn_validate(ctypes.byref(F)), "moe_ffn_validate")
+        lib = load_library()
+        _check(lib.moe_ffn_validate(ctypes.byref(F)), "moe_ffn_validate")
+        F.call = ((T, self.d), (2, T, self.f), self.dtype, self.device.index, ctypes.byref(F),
+                  lib.moe_ffn_forward, lib.moe_ffn_backward)
         return F
 
 
@@ -565,34 +560,29 @@ def ffn_pre(F: MoeFfn, device=None):
     return torch.empty((2, F.T, F.f), dtype=torch.float32, device=device or F.owner.device)
 
 
-def _check_pre(F: MoeFfn, pre):
+def _check_pre(pre, shape, index):
     import torch
-    if pre.dtype != torch.float32 or pre.shape != (2, F.T, F.f) or \
-            pre.device != F.owner.device or not pre.is_contiguous():
-        raise ValueError(f"pre: expected contiguous fp32 [2, {F.T}, {F.f}] on {F.owner.device}")
-
-
-def _check_dense(F: MoeFfn, t, name, rows, cols):
-    if t.dtype != F.owner.dtype or t.device != F.owner.device or t.shape != (rows, cols) or \
-            not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {F.owner.dtype} [{rows}, {cols}] on "
-                         f"{F.owner.device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if pre.dtype != torch.float32 or pre.shape != shape or pre.get_device() != index or \
+            not pre.is_contiguous():
+        raise ValueError(f"pre: expected contiguous fp32 {list(shape)} on cuda:{index}")
 
 
 def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     """y = Wd (act(Wg x) * (Wu x)) for the rows of x [T, d]; ``pre`` (ffn_pre) keeps what
     ffn_backward needs (include/moe_b200.h)."""
-    dev = F.owner.device
-    _check_dense(F, x, "x", F.T, F.d)
+    shape, pre_shape, dtype, index, ref, fn, _ = F.call
+    _check_rows(x, "x", shape, dtype, index)
     if out is None:
-        out = x.new_empty((F.T, F.d))
+        out = x.new_empty(shape)
     else:
-        _check_dense(F, out, "out", F.T, F.d)
+        _check_rows(out, "out", shape, dtype, index)
     if pre is not None:
-        _check_pre(F, pre)
-    _check_ws(ws, dev)
-    _check(_call(dev, stream, load_library().moe_ffn_forward, ctypes.byref(F), x.data_ptr(),
-                 out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel()), "moe_ffn_forward")
+        _check_pre(pre, pre_shape, index)
+    _check_ws(ws, index)
+    status = _call(index, stream, fn, ref, x.data_ptr(), out.data_ptr(), _ptr(pre), ws.data_ptr(),
+                   ws.numel())
+    if status:
+        _check(status, "moe_ffn_forward")
     return out
 
 
@@ -600,25 +590,24 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
                  stream=None):
     """(dx, dw_gate, dw_up, dw_down) from dy [T, d], x and the ``pre`` of ffn_forward; what is
     not needed is None and not computed. ``ws``: alloc_ffn_workspace(F, backward=True)."""
-    dev = F.owner.device
-    _check_dense(F, x, "x", F.T, F.d)
-    _check_dense(F, dy, "dy", F.T, F.d)
-    _check_pre(F, pre)
-    _check_ws(ws, dev)
-    dx = x.new_empty((F.T, F.d)) if need_dx else None
+    shape, pre_shape, dtype, index, ref, _, fn = F.call
+    _check_rows(x, "x", shape, dtype, index)
+    _check_rows(dy, "dy", shape, dtype, index)
+    _check_pre(pre, pre_shape, index)
+    _check_ws(ws, index)
+    dx = x.new_empty(shape) if need_dx else None
     dwg = dwu = dwd = None
     if need_dw:
         dwg, dwu = x.new_empty((F.f, F.d)), x.new_empty((F.f, F.d))
         dwd = x.new_empty((F.d, F.f))
-    _check(_call(dev, stream, load_library().moe_ffn_backward, ctypes.byref(F), x.data_ptr(),
-                 dy.data_ptr(), pre.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd),
-                 ws.data_ptr(), ws.numel()), "moe_ffn_backward")
+    _check(_call(index, stream, fn, ref, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), _ptr(dx),
+                 _ptr(dwg), _ptr(dwu), _ptr(dwd), ws.data_ptr(), ws.numel()), "moe_ffn_backward")
     return dx, dwg, dwu, dwd
 
 
 def _device_status(fn, D, ws, stream):
     code, site = ctypes.c_int32(0), ctypes.c_int32(0)
-    _check(_call(D.owner.device, stream, fn, ctypes.byref(D), ws.data_ptr(), ws.numel(),
+    _check(_call(D.owner.device.index, stream, fn, ctypes.byref(D), ws.data_ptr(), ws.numel(),
                  ctypes.byref(code), ctypes.byref(site)), fn.__name__)
     return code.value, site.value
 

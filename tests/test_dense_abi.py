@@ -92,11 +92,18 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError):
         binding.QuantMatrix(codes, torch.zeros(4, 1, dtype=torch.bfloat16), 130)
     x = torch.zeros(4, 8, dtype=torch.bfloat16)
-    dev = x.device
-    binding._check_rows(x, "x", 4, 8, torch.bfloat16, dev)
-    for t in (x[:, ::2], x.T, x.float(), x[:3], x[:1].expand(4, 8)):
+    check = lambda t, stride=None: binding._check_rows(  # noqa: E731 (-1: the CPU's index)
+        t, "x", (4, 8), torch.bfloat16, -1, stride)
+    check(x)
+    wide = torch.zeros(4, 24, dtype=torch.bfloat16)
+    check(wide[:, :8], 24)
+    for t in (wide[:, :8], wide[:, ::3], x.T, x.float(), x[:3], x[:1].expand(4, 8), x[None]):
         with pytest.raises(ValueError):
-            binding._check_rows(t, "x", 4, 8, torch.bfloat16, dev)
+            check(t)
+    with pytest.raises(ValueError):
+        check(x, 24)
+    with pytest.raises(ValueError):
+        binding._check_rows(x, "x", (4, 8), torch.bfloat16, 0)
 
 
 def ffn(fmt=16, **kw):
