@@ -17,6 +17,11 @@ int device_sms();
 // `done` is the kernel's own array of kMaxDevices flags.
 cudaError_t allow_smem(const void* kernel, bool* done);
 
+// Starts the fetch of a tensor map (a kernel's first TMA copy waits for its map otherwise).
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ------------------------------------------------------------------ activations
 
 // Both activations are g sigma(k): silu with k = g, gelu in its tanh form with

@@ -293,6 +293,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1;
 
+  if (warp == 2 && lane < a.n) {  // the maps of the first copies
+    prefetch_map(&a.p[lane].a[0]);
+    prefetch_map(&a.p[lane].b[EPI == EPI_GATED ? rank : 0]);
+  }
+  if (warp == 3 && lane < (EPI == EPI_STORE ? a.n : EPI == EPI_GATED ? (a.keep ? 3 : 1) : 5))
+    prefetch_map(&a.o[lane]);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&full[s], 1);
@@ -470,16 +476,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const size_t my = ((size_t)rank * kEpiWarps + (warp - 2)) * (ACC / 4) * 32 + lane;
         float4* base = reinterpret_cast<float4*>(a.partial);
         float4* dst = base + (size_t)u.unit * unit_f4 + my;
+        constexpr int NC = ACC < 64 ? ACC / 16 : 4;  // chunks of 16 columns at a time
 #pragma unroll 1
-        for (int c = 0; c < ACC; c += 16) {
-          uint32_t r[16];
-          tmem_ld16_async(acc_addr(c), r);
+        for (int c = 0; c < ACC; c += 16 * NC) {
+          uint32_t r[NC][16];
+#pragma unroll
+          for (int i = 0; i < NC; ++i) tmem_ld16_async(acc_addr(c + 16 * i), r[i]);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            __stcg(dst + (c / 4 + j) * 32,
-                   make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              __stcg(dst + (c / 4 + 4 * i + j) * 32,
+                     make_float4(__uint_as_float(r[i][4 * j]), __uint_as_float(r[i][4 * j + 1]),
+                                 __uint_as_float(r[i][4 * j + 2]),
+                                 __uint_as_float(r[i][4 * j + 3])));
         }
         __threadfence();
         __syncwarp();

@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   uint4* xs = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(bars) + 1024);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < (GATED ? 2 : 1)) prefetch_map(&maps.w[threadIdx.x]);
   const int t4 = lane & 3;
   // the tile row of MMA row lane / 4: two rows that one phase of a 16-byte read covers lie four
   // apart, where the 128-byte swizzle gives them different banks
