@@ -15,12 +15,19 @@
 // a slot, 16 rows x 128 bytes, into its warp's own ring in shared memory by TMA (whole lines:
 // boxes of 64 bytes reach 5.7 TB/s, of 128 bytes 6.5), 2 to 6 slots ahead of the products.
 //
-// Products: mma.sync m16n8k16, 8 activation rows wide. The int4 codes enter exactly, as the
-// 16-bit values (136 + q) - 136 (bf16) or (1032 + q) - 1032 (fp16): one LOP3 and one packed
-// subtraction for two codes. Subtracting before the product instead of correcting the sum
-// keeps infinities in x infinite and costs only the FMA pipe, which is otherwise idle (the
-// ALU pipe, 7 operations for 8 codes at half rate, is the busiest). A group's products are
-// summed in fp32 by the tensor core, then acc += s * sum in fp32.
+// Products: mma.sync m16n8k16, 8 activation rows wide, int4 codes exact in one of two forms.
+//   masked  the nibbles of q + 8 as they lie in the word, at bits 0..3 or 4..7 of a 16-bit half:
+//           as bf16 or fp16 bits that is (q + 8) or 16 (q + 8) times the smallest subnormal
+//           (bits below 256 count it linearly in both types), so one LOP3 makes two codes and
+//           one shift a word is left. bf16 rows are taken times 2^100, which keeps every
+//           product a normal fp32 number. The sums start at -8 sum(x) of the group (computed
+//           once a CTA by the same instructions), so they end at sum(q x).
+//   offset  (136 + q) - 136 in bf16, (1032 + q) - 1032 in fp16: three shifts a word and a packed
+//           subtraction for two codes, 48 instructions of 180 for 128 x 16 codes more. It has
+//           no offset to cancel and no range, so a call whose rows hold infinities, NaN, or
+//           bf16 magnitudes outside [2^-90, 2^26) takes it (each CTA sees that while it stages
+//           the rows), and so do calls that it does not pay (kMaskedUnits).
+// A group's products are summed in fp32 by the tensor core, then acc += s * sum in fp32.
 //
 // The activation rows sit in shared memory in fragment order, staged once per CTA. Columns of
 // the MMA beyond the last row repeat or hold anything: they are never stored. Rows that do not
@@ -28,6 +35,7 @@
 // the CTA that brings the last one adds them in part order, so the result does not depend on
 // the order of arrival.
 #include <cstring>
+#include <type_traits>
 
 #include "dense.cuh"
 #include "tc_common.cuh"
@@ -42,6 +50,11 @@ constexpr int kSlotBytes = 2048;                 // 16 rows x 128 bytes
 constexpr int kRingSlot = kWarps * kSlotBytes;   // one slot of every warp's ring
 constexpr int kMaxDepth = 6;
 constexpr int kSiteGemvSlot = 60;
+// The masked form from so many 16-row x 128-code units on. Its sums and its look at the rows cost
+// a call 0.3 us: 1024 x 2560 (1280 units) 4.5 us against 4.2, 10240 x 2560 (12800) 8.8 against
+// 9.3, 131072 x 2560 39.7 against 45.9. With groups of 32 four starts a unit cost more than they
+// save (20480 x 4096 22.0 us against 21.1), with 16 rows likewise (10240 x 2560 12.1 against 11.5).
+constexpr long long kMaskedUnits = 8192;
 
 // K is counted in units of 64 bytes of a weight row (128 int4 or 32 16-bit values): what 8 (2)
 // MMAs multiply. A slot holds two.
@@ -56,6 +69,8 @@ struct GemvPlan {
   int tiles_q, tiles_r;
   int tc;            // 8-row column tiles
   int cols;          // activation rows staged (an even number; whole column tiles above one)
+  int masked;        // the masked form where the rows allow it
+  int sums;          // bytes of a unit's group sums
   int wpr;           // log2 of the warps that stage one row
   int depth;         // ring slots a warp
   int pdl;           // launched to overlap the kernel before it
@@ -70,7 +85,11 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   p.cols = p.tc == 1 ? (a.T + 1) & ~1 : 8 * p.tc;
   p.rows = a.gated ? 8 : 16;
   p.tiles = (a.N + p.rows - 1) / p.rows;
-  const int unit_bytes = p.unit_k * 2 * p.cols;
+  // a unit's rows, and (the masked form) its groups' sums
+  p.masked = a.fmt == 4 && a.group == 128 && p.tc == 1 &&
+             (long long)p.tiles * p.units >= kMaskedUnits;
+  p.sums = p.masked ? 8 * 4 : 0;
+  const int unit_bytes = p.unit_k * 2 * p.cols + p.sums;
   const int room = kSmemMax - 2048;                // beside the staged rows: two slots a warp
   const int fit = std::max(2, (room - 2 * kRingSlot) / unit_bytes & ~1);
   p.parts = (p.units + fit - 1) / fit;
@@ -113,8 +132,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   }
 }
 
-// Nibbles 0 and 4 of w as an exact pair of 16-bit values: the code with its sign bit flipped
-// in the mantissa of 128 (bf16) or 1024 (fp16), minus that offset plus 8.
+// The offset form. Nibbles 0 and 4 of w as an exact pair of 16-bit values: the code with its
+// sign bit flipped in the mantissa of 128 (bf16) or 1024 (fp16), minus that offset plus 8.
 template <bool F16> __device__ __forceinline__ uint32_t codes_pair(uint32_t w) {
   constexpr uint32_t kOff = F16 ? 0x64086408u : 0x43084308u;
   uint32_t r;
@@ -126,6 +145,33 @@ template <bool F16> __device__ __forceinline__ uint32_t codes_pair(uint32_t w) {
   }
   return r;
 }
+
+// The masked form: nibbles (w & mask) with their sign bits flipped.
+__device__ __forceinline__ uint32_t masked_codes(uint32_t w, uint32_t mask, uint32_t flip) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(mask), "r"(flip));  // (a & b) ^ c
+  return r;
+}
+constexpr uint32_t kLow = 0x000F000Fu, kLow8 = 0x00080008u;    // bits 0..3: q + 8
+constexpr uint32_t kHigh = 0x00F000F0u, kHigh8 = 0x00800080u;  // bits 4..7: 16 (q + 8)
+
+// Range of the rows' magnitudes over packed 16-bit halves: the largest, and the smallest that
+// is not zero, minus one.
+struct Range16 {
+  uint32_t hi = 0, lo = 0xffffffffu;
+  __device__ __forceinline__ void add(uint32_t w) {
+    const uint32_t m = w & 0x7fff7fffu;
+    uint32_t d;
+    asm("max.u16x2 %0, %0, %1;" : "+r"(hi) : "r"(m));
+    asm("add.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(0xffffffffu));
+    asm("min.u16x2 %0, %0, %1;" : "+r"(lo) : "r"(d));
+  }
+  // bf16: below 2^26 and at least 2^-90; fp16: finite.
+  template <bool F16> __device__ __forceinline__ bool inside() const {
+    const uint32_t h = max(hi & 0xffffu, hi >> 16), l = min(lo & 0xffffu, lo >> 16);
+    return F16 ? h < 0x7C00u : h < 0x4C80u && l >= 0x1280u - 1;
+  }
+};
 
 // Where word group i of lane t of an int4 slot lies (16-byte chunk, word in it), and the
 // inverse for staging x: chunk c8 of 8 K values of a slot -> (i, t). Each MMA pair i of a slot
@@ -147,7 +193,9 @@ template <int GROUP> __device__ __forceinline__ void place_of(int w, int* i, int
   }
 }
 
-template <int FMT, int GROUP, bool F16, int TC, bool GATED>
+// MASKED: has the masked form too (a kernel of its own: the second loop costs small calls 0.5 us
+// of instruction fetches).
+template <int FMT, int GROUP, bool F16, int TC, bool GATED, bool MASKED>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     gemv_rows_kernel(const __grid_constant__ GemvMaps maps, const GemvArgs a, const GemvPlan p) {
   constexpr int XI = FMT == 4 ? 4 : 1;             // 16-byte fragment chunks a lane and unit
@@ -238,8 +286,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int xstride = 32 << p.wpr;
   const int xstart = lane + 32 * (warp & ((1 << p.wpr) - 1));
   const int xwrap = (max(0, nc - xstart) + xstride - 1) & ~(xstride - 1);
-  int xrow = warp >> p.wpr, xc = xstart;
-  const uint4* xsrc = reinterpret_cast<const uint4*>(a.x + (size_t)xrow * a.ldx) + c0;
+  int xrow = 0, xc = 0;
+  const uint4* xsrc = nullptr;
+  auto x_start = [&]() {
+    xrow = warp >> p.wpr;
+    xc = xstart;
+    xsrc = reinterpret_cast<const uint4*>(a.x + (size_t)xrow * a.ldx) + c0;
+  };
+  x_start();
+  Range16 range;
   const size_t xrow_step = (size_t)(kWarps >> p.wpr) * (a.ldx / 8);
   uint4 xv[XB];
   int xat[XB];                                     // row in the upper half, chunk in the lower
@@ -258,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       xc += xstride;
     }
   };
-  auto put_x = [&]() {
+  auto put_x = [&](bool masked) {
 #pragma unroll
     for (int j = 0; j < XB; ++j) {
       if (xat[j] < 0) continue;
@@ -267,11 +322,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       uint4 w = xv[j];
       if constexpr (FMT == 4) {
         place_of<GROUP>(c % UNIT_CHUNKS, &fi, &ft);
-        // (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
+        // (0,1) (2,3) (4,5) (6,7) -> (0,4) (2,6) (1,5) (3,7)
         w.x = __byte_perm(xv[j].x, xv[j].z, 0x5410);
-        w.y = __byte_perm(xv[j].x, xv[j].z, 0x7632);
-        w.z = __byte_perm(xv[j].y, xv[j].w, 0x5410);
+        w.y = __byte_perm(xv[j].y, xv[j].w, 0x5410);
+        w.z = __byte_perm(xv[j].x, xv[j].z, 0x7632);
         w.w = __byte_perm(xv[j].y, xv[j].w, 0x7632);
+        if (MASKED && masked) {
+          range.add(w.x), range.add(w.y), range.add(w.z), range.add(w.w);
+          if constexpr (!F16) {
+            constexpr uint32_t k100 = 0x71807180u;  // 2^100
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(k100));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(k100));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w.z) : "r"(k100));
+            asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w.w) : "r"(k100));
+          }
+        }
       }
       // neighbouring rows change places in odd chunk rows, halves of 64 bytes in chunks 2 and 3:
       // eight neighbouring chunks of a row then lie in different banks
@@ -288,12 +353,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   pdl_trigger();
   fetch_x();
   if (!p.pdl) start_ring();
-  put_x();
+  put_x(MASKED);
   while (xrow < a.T) {
     fetch_x();
-    put_x();
+    put_x(MASKED);
   }
-  __syncthreads();
+  bool masked = false;
+  if constexpr (MASKED) {
+    masked = !__syncthreads_or(!range.template inside<F16>());
+    if (!masked) {                                 // (rare) the rows again, as they are
+      x_start();
+      while (xrow < a.T) {
+        fetch_x();
+        put_x(false);
+      }
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
 
   // this lane's column (beyond the last row of a single column tile: the last one again)
   const int col = TC == 1 ? min(lane >> 2, a.T - 1) : lane >> 2;
@@ -304,6 +382,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   // 16 bytes of chunk c (0..7, units of 64 bytes side by side) of this lane's row, swizzled
   const uint32_t chunk_row = (uint32_t)g * 128;
   auto chunk_at = [&](int c) -> uint32_t { return chunk_row + ((c ^ g) << 4); };
+
+  // ---- the masked form's start of a group: -8 sum(x), [unit][group][column], a warp a unit
+  float* sums = reinterpret_cast<float*>(xs) + (size_t)p.part_units * XI * p.cols * 16;
+  if (MASKED && masked) {
+    for (int un = warp; un < n_units; un += kWarps) {
+      float c[TC][2][4];
+      const uint8_t* xp = xlane + un * XI * xstep;
+#pragma unroll
+      for (int i = 0; i < XI; ++i) {
+        constexpr int kWords = GROUP / 32;  // words a group
+#pragma unroll
+        for (int n = 0; n < TC; ++n) {
+          const uint4 x4 = *reinterpret_cast<const uint4*>(
+              xp + n * 512 + ((i & 1) ? xflip : 0) + ((i & 2) ? xswap : 0));
+          if (i % kWords == 0) {
+            mma16816<F16, true>(c[n][0], kLow8, kLow8, kLow8, kLow8, x4.x, x4.y);
+            mma16816<F16, true>(c[n][1], kHigh8, kHigh8, kHigh8, kHigh8, x4.z, x4.w);
+          } else {
+            mma16816<F16>(c[n][0], kLow8, kLow8, kLow8, kLow8, x4.x, x4.y);
+            mma16816<F16>(c[n][1], kHigh8, kHigh8, kHigh8, kHigh8, x4.z, x4.w);
+          }
+          if (i % kWords == kWords - 1 && lane < 4)
+            *reinterpret_cast<float2*>(sums + ((un * NSC + i / kWords) * TC + n) * 8 + 2 * t4) =
+                make_float2(-fmaf(0.0625f, c[n][1][0], c[n][0][0]),
+                            -fmaf(0.0625f, c[n][1][1], c[n][0][1]));
+        }
+        xp += xstep;
+      }
+    }
+    __syncthreads();
+  }
 
   // ---- one tile's sums to the output
   const int esize = a.y32 ? 4 : 2;
@@ -363,103 +472,139 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[c][j] = head[c][j] = 0.f;
   const uint8_t* xp = xlane + slot0 * (2 * XI) * xstep;
-  for (int it = 0; it < n_my; ++it) {
-    uint32_t sc[NSC];
+  // 2^133 / 2^100 (bf16) or 2^24 (fp16): the masked form's unit
+  const float unit = !(MASKED && masked) ? 1.f : F16 ? 16777216.f : 8589934592.f;
+  auto run = [&](auto fast) {
+    constexpr bool FAST = decltype(fast)::value;
+    for (int it = 0; it < n_my; ++it) {
+      float sc[NSC];
 #pragma unroll
-    for (int j = 0; j < NSC; ++j) sc[j] = sn[j] << 16;
-    load_scales();
-    const uint8_t* sp = ring + stage * kSlotBytes;
-    if (ok && !mbar_wait(&full[stage], phase)) {
-      set_timeout(a.status, kSiteGemvSlot);
-      ok = false;
-    }
-    const bool two = 2 * slot + 1 < n_units;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (u == 1 && !two) break;
-      uint32_t wa[4], wb[4];
-      if constexpr (FMT == 16 || GROUP == 128) {
-        const uint32_t at = chunk_at(4 * u + t4);
-        const uint4 ua = *reinterpret_cast<const uint4*>(sp + at);
-        const uint4 ub = *reinterpret_cast<const uint4*>(sp + 1024 + at);
-        wa[0] = ua.x, wa[1] = ua.y, wa[2] = ua.z, wa[3] = ua.w;
-        wb[0] = ub.x, wb[1] = ub.y, wb[2] = ub.z, wb[3] = ub.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int w = word_of<GROUP>(i, t4);
-          const uint32_t at = chunk_at(4 * u + (w >> 2)) + (w & 3) * 4;
-          wa[i] = *reinterpret_cast<const uint32_t*>(sp + at);
-          wb[i] = *reinterpret_cast<const uint32_t*>(sp + 1024 + at);
-        }
+      for (int j = 0; j < NSC; ++j) {
+        sc[j] = __uint_as_float(sn[j] << 16);
+        if constexpr (FAST) sc[j] *= unit;
       }
-      if (u == 1 || !two) {                        // the slot is read: bring the next one
-        __syncwarp();
-        if (++stage == p.depth) {
-          stage = 0;
-          phase ^= 1;
-        }
-        copy_next();
+      load_scales();
+      const uint8_t* sp = ring + stage * kSlotBytes;
+      if (ok && !mbar_wait(&full[stage], phase)) {
+        set_timeout(a.status, kSiteGemvSlot);
+        ok = false;
       }
-      if constexpr (FMT == 16) {
+      const bool two = 2 * slot + 1 < n_units;
 #pragma unroll
-        for (int n = 0; n < TC; ++n) {
-          const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512 + (u ? xflip : 0));
-          mma16816<F16>(acc[n], wa[0], wb[0], wa[1], wb[1], x4.x, x4.y);
-          mma16816<F16>(acc[n], wa[2], wb[2], wa[3], wb[3], x4.z, x4.w);
+      for (int u = 0; u < 2; ++u) {
+        if (u == 1 && !two) break;
+        uint32_t wa[4], wb[4];
+        if constexpr (FMT == 16 || GROUP == 128) {
+          const uint32_t at = chunk_at(4 * u + t4);
+          const uint4 ua = *reinterpret_cast<const uint4*>(sp + at);
+          const uint4 ub = *reinterpret_cast<const uint4*>(sp + 1024 + at);
+          wa[0] = ua.x, wa[1] = ua.y, wa[2] = ua.z, wa[3] = ua.w;
+          wb[0] = ub.x, wb[1] = ub.y, wb[2] = ub.z, wb[3] = ub.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int w = word_of<GROUP>(i, t4);
+            const uint32_t at = chunk_at(4 * u + (w >> 2)) + (w & 3) * 4;
+            wa[i] = *reinterpret_cast<const uint32_t*>(sp + at);
+            wb[i] = *reinterpret_cast<const uint32_t*>(sp + 1024 + at);
+          }
         }
-        xp += xstep;
-      } else {
-        float c[TC][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          constexpr int kWords = GROUP / 32;  // words a group
-          const uint32_t a0 = codes_pair<F16>(wa[i]), a1 = codes_pair<F16>(wb[i]);
-          const uint32_t a2 = codes_pair<F16>(wa[i] >> 4), a3 = codes_pair<F16>(wb[i] >> 4);
-          const uint32_t a4 = codes_pair<F16>(wa[i] >> 8), a5 = codes_pair<F16>(wb[i] >> 8);
-          const uint32_t a6 = codes_pair<F16>(wa[i] >> 12), a7 = codes_pair<F16>(wb[i] >> 12);
+        if (u == 1 || !two) {                        // the slot is read: bring the next one
+          __syncwarp();
+          if (++stage == p.depth) {
+            stage = 0;
+            phase ^= 1;
+          }
+          copy_next();
+        }
+        if constexpr (FMT == 16) {
 #pragma unroll
           for (int n = 0; n < TC; ++n) {
-            const uint4 x4 = *reinterpret_cast<const uint4*>(
-                xp + n * 512 + ((i & 1) ? xflip : 0) + ((i & 2) ? xswap : 0));
-            if (i % kWords == 0) mma16816<F16, true>(c[n], a0, a1, a2, a3, x4.x, x4.y);
-            else mma16816<F16>(c[n], a0, a1, a2, a3, x4.x, x4.y);
-            mma16816<F16>(c[n], a4, a5, a6, a7, x4.z, x4.w);
+            const uint4 x4 = *reinterpret_cast<const uint4*>(xp + n * 512 + (u ? xflip : 0));
+            mma16816<F16>(acc[n], wa[0], wb[0], wa[1], wb[1], x4.x, x4.y);
+            mma16816<F16>(acc[n], wa[2], wb[2], wa[3], wb[3], x4.z, x4.w);
           }
           xp += xstep;
-          if (i % kWords == kWords - 1) {
-            const float s0 = __uint_as_float(__shfl_sync(0xffffffffu, sc[i / kWords], u, 4));
-            const float s1 = __uint_as_float(__shfl_sync(0xffffffffu, sc[i / kWords], 2 + u, 4));
+        } else {
+          float c[TC][4], ch[FAST ? TC : 1][4];
+          const float* start = sums + ((2 * slot + u) * NSC * TC) * 8 + 2 * t4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            constexpr int kWords = GROUP / 32;  // words a group
+            uint32_t al[4], ah[4];              // codes 0, 4 | 2, 6 and 1, 5 | 3, 7 of both rows
+            if constexpr (FAST) {
+              const uint32_t va = wa[i] >> 8, vb = wb[i] >> 8;
+              al[0] = masked_codes(wa[i], kLow, kLow8), al[1] = masked_codes(wb[i], kLow, kLow8);
+              al[2] = masked_codes(va, kLow, kLow8), al[3] = masked_codes(vb, kLow, kLow8);
+              ah[0] = masked_codes(wa[i], kHigh, kHigh8), ah[1] = masked_codes(wb[i], kHigh, kHigh8);
+              ah[2] = masked_codes(va, kHigh, kHigh8), ah[3] = masked_codes(vb, kHigh, kHigh8);
+            } else {
+              al[0] = codes_pair<F16>(wa[i]), al[1] = codes_pair<F16>(wb[i]);
+              al[2] = codes_pair<F16>(wa[i] >> 8), al[3] = codes_pair<F16>(wb[i] >> 8);
+              ah[0] = codes_pair<F16>(wa[i] >> 4), ah[1] = codes_pair<F16>(wb[i] >> 4);
+              ah[2] = codes_pair<F16>(wa[i] >> 12), ah[3] = codes_pair<F16>(wb[i] >> 12);
+            }
 #pragma unroll
             for (int n = 0; n < TC; ++n) {
-              acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
-              acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
-              acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
-              acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
+              const uint4 x4 = *reinterpret_cast<const uint4*>(
+                  xp + n * 512 + ((i & 1) ? xflip : 0) + ((i & 2) ? xswap : 0));
+              if constexpr (FAST) {
+                if (i % kWords == 0) {
+                  const float2 s8 =
+                      *reinterpret_cast<const float2*>(start + (i / kWords * TC + n) * 8);
+                  c[n][0] = c[n][2] = s8.x;
+                  c[n][1] = c[n][3] = s8.y;
+                  mma16816<F16, true>(ch[n], ah[0], ah[1], ah[2], ah[3], x4.z, x4.w);
+                } else {
+                  mma16816<F16>(ch[n], ah[0], ah[1], ah[2], ah[3], x4.z, x4.w);
+                }
+                mma16816<F16>(c[n], al[0], al[1], al[2], al[3], x4.x, x4.y);
+              } else {
+                if (i % kWords == 0) mma16816<F16, true>(c[n], al[0], al[1], al[2], al[3], x4.x, x4.y);
+                else mma16816<F16>(c[n], al[0], al[1], al[2], al[3], x4.x, x4.y);
+                mma16816<F16>(c[n], ah[0], ah[1], ah[2], ah[3], x4.z, x4.w);
+              }
+            }
+            xp += xstep;
+            if (i % kWords == kWords - 1) {
+              const float s0 = __shfl_sync(0xffffffffu, sc[i / kWords], u, 4);
+              const float s1 = __shfl_sync(0xffffffffu, sc[i / kWords], 2 + u, 4);
+#pragma unroll
+              for (int n = 0; n < TC; ++n) {
+                if constexpr (FAST)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) c[n][j] = fmaf(0.0625f, ch[n][j], c[n][j]);
+                acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
+                acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
+                acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
+                acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
+              }
             }
           }
         }
       }
-    }
-    if (++slot == n_slots) {
-      if (whole) {
-        finish(tile, acc);
-      } else {
+      if (++slot == n_slots) {
+        if (whole) {
+          finish(tile, acc);
+        } else {
+#pragma unroll
+          for (int c = 0; c < TC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) head[c][j] = acc[c][j];
+        }
+        slot = 0;
+        ++tile;
+        whole = true;
+        xp = xlane;
 #pragma unroll
         for (int c = 0; c < TC; ++c)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) head[c][j] = acc[c][j];
+          for (int j = 0; j < 4; ++j) acc[c][j] = 0.f;
       }
-      slot = 0;
-      ++tile;
-      whole = true;
-      xp = xlane;
-#pragma unroll
-      for (int c = 0; c < TC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[c][j] = 0.f;
     }
-  }
+  };
+  if (MASKED && masked) run(std::integral_constant<bool, MASKED>{});
+  else run(std::false_type{});
 
   // ---- tiles that several warps share: each leaves the sums of the tile it did not begin
   // ("head") in its ring, which nothing is on its way into any more; the warp that began a tile
@@ -534,9 +679,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-template <int FMT, int GROUP, bool F16, int TC, bool GATED>
+template <int FMT, int GROUP, bool F16, int TC, bool GATED, bool MASKED = false>
 cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
-  auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED>;
+  auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED, MASKED>;
   static bool done[kMaxDevices] = {};
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
   if (err != cudaSuccess) return err;
@@ -563,7 +708,10 @@ cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bo
 template <int FMT, int GROUP, bool F16, bool GATED>
 cudaError_t launch_tc(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
   switch (p.tc) {
-    case 1: return launch_one<FMT, GROUP, F16, 1, GATED>(a, p, st, pdl);
+    case 1:
+      if constexpr (FMT == 4 && GROUP == 128)
+        if (p.masked) return launch_one<FMT, GROUP, F16, 1, GATED, true>(a, p, st, pdl);
+      return launch_one<FMT, GROUP, F16, 1, GATED>(a, p, st, pdl);
     case 2: return launch_one<FMT, GROUP, F16, 2, GATED>(a, p, st, pdl);
     case 3: return launch_one<FMT, GROUP, F16, 3, GATED>(a, p, st, pdl);
     default: return launch_one<FMT, GROUP, F16, 4, GATED>(a, p, st, pdl);

@@ -303,7 +303,10 @@ MOE_API moe_status moe_nvfp4_quantize_rows(const float* v, int32_t rows, int32_t
  *   y[t][n] = sum_k q[n][k] * s[n][k / group] * x[t][k] (+ bias[n])
  * in the MOE_W_INT4 encoding (codes uint32 [N][K / 8], scales bf16 [N][K / group]). Each
  * group's products are summed in fp32 with the codes exact, the group sums in fp32 times
- * their scale, and the result is rounded once to y_type.
+ * their scale, and the result is rounded once to y_type. Large matrices with groups of 128
+ * and up to 8 rows sum (q + 8) x and take 8 sum(x) off (both in fp32, so their rounding is
+ * relative to (|q| + 8) |x|), unless the rows hold infinities, NaN, or bf16 magnitudes
+ * outside [2^-90, 2^26).
  * 1 <= T <= 32, N >= 1, group 32, 64 or 128, K % group == 0, 1 <= K <= 32768, N <= 2^24. x_type
  * MOE_T_BF16 or MOE_T_FP16; y_type x_type or MOE_T_FP32. ldx, ldy: elements between rows
  * (ldx >= K and a multiple of 8, ldy >= N). w and x 16-byte aligned, s 2, y 4 for fp32 and

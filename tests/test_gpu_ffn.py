@@ -155,7 +155,7 @@ def test_gradients_match_differences(B, act):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("T,d,f", [(1, 128, 128), (1, 2560, 1024), (3, 256, 384), (8, 640, 256),
-                                   (9, 384, 1280), (16, 2560, 512), (17, 128, 2560),
+                                   (9, 384, 1280), (16, 2560, 512), (17, 128, 2560), (2, 2560, 4096), (7, 4096, 2560),
                                    (32, 2560, 2560)])
 def test_int4_block_matches_64_bits(B, T, d, f, act):
     block, W = make(B, d, f, fmt="int4", act=act, seed=d + f)

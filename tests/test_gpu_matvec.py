@@ -52,9 +52,91 @@ def test_matches_64_bits(B, T, N, K, group, x_dtype, y_dtype):
     xd = x.cuda()
     y = B.matvec(desc, xd, ws)
     y2 = B.matvec(desc, xd, ws)  # the same workspace again: its counters are back at zero
+    assert B.matvec_device_status(desc, ws) == (0, 0)
     assert y.dtype == y_dtype and tuple(y.shape) == (T, N)
     assert torch.equal(y, y2)
     check(y, x, W, b, group, f"{T}x{N}x{K} g{group}")
+
+
+# ---- calls large enough for the products on shifted codes (few rows, groups of 128): the sums
+# are sum((q + 8) x) - 8 sum(x), so their terms' magnitudes are those of |q| + 8
+
+BIG = (40000, 640)  # N, K: an odd number of groups
+
+
+def check_shifted(y, x, W, scales, what=""):
+    ref, _ = matvec_ref(x, W)
+    W8 = W.abs() + 8 * scales.double().repeat_interleave(128, 1)
+    bound = (x.double().abs() @ W8.T) * matvec_additions(W.shape[1], 128) * 2.0 ** -23
+    return assert_close(y, ref, bound, y.dtype, what)
+
+
+@pytest.fixture(scope="module")
+def big(B):
+    gen = torch.Generator().manual_seed(11)
+    N, K = BIG
+    codes, scales = quantise(gen, N, K, 128)
+    codes[5] = 0                                    # a row of zero codes
+    return B.QuantMatrix(codes.cuda(), scales.cuda(), K), dequantise(codes, scales, 128), scales
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8])
+@pytest.mark.parametrize("x_dtype,y_dtype", [(BF, F32), (HF, F32), (BF, BF), (HF, HF)])
+def test_large_matrix_few_rows(B, big, T, x_dtype, y_dtype):
+    m, W, scales = big
+    gen = torch.Generator().manual_seed(T)
+    x = torch.randn(T, BIG[1], generator=gen).to(x_dtype)
+    desc = m.descriptor(T, x_dtype=x_dtype, y_dtype=y_dtype)
+    ws = B.alloc_matvec_workspace(desc)
+    y = B.matvec(desc, x.cuda(), ws)
+    assert torch.equal(y, B.matvec(desc, x.cuda(), ws))
+    check_shifted(y, x, W, scales)
+    assert B.matvec_device_status(desc, ws) == (0, 0)
+
+
+@pytest.mark.parametrize("value", [2.0 ** 25, 2.0 ** 26, 2.0 ** 100, 2.0 ** -90, 2.0 ** -91, 2.0 ** -120,
+                                   2.0 ** -133])
+def test_large_matrix_magnitudes_at_the_ends_of_the_range(B, big, value):
+    """Rows whose bf16 magnitudes reach the ends of the shifted form's range, and leave it."""
+    m, W, scales = big
+    x = torch.zeros(1, BIG[1], dtype=BF)
+    x[0, ::3] = value
+    x[0, 1::6] = -value
+    desc = m.descriptor(1, y_dtype=F32)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+    check_shifted(y, x, W, scales)
+    # beside ordinary values: a term of every size counts
+    x2 = x.clone()
+    x2[0, 2] = 1.0
+    y = B.matvec(desc, x2.cuda(), B.alloc_matvec_workspace(desc))
+    check_shifted(y, x2, W, scales)
+
+
+@pytest.mark.parametrize("x_dtype", [BF, HF])
+def test_large_matrix_infinities_and_nan(B, big, x_dtype):
+    m, W, scales = big
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(3, BIG[1], generator=gen).to(x_dtype)
+    x[1, 300], x[2, 7] = float("inf"), float("nan")
+    desc = m.descriptor(3, x_dtype=x_dtype, y_dtype=F32)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc)).cpu()
+    check_shifted(y[:1], x[:1], W, scales)
+    w = W[:, 300]
+    assert torch.isnan(y[1][w == 0]).all() and torch.isnan(y[2]).all()
+    assert torch.equal(y[1][w != 0].double(), torch.sign(w[w != 0]) * float("inf"))
+
+
+@pytest.mark.parametrize("x_dtype", [BF, HF])
+def test_large_matrix_single_weights(B, big, x_dtype):
+    """One-hot rows through the shifted form are exact too: both terms are small integers times
+    the one activation."""
+    m, W, _ = big
+    for k0 in (0, 121, 256, 632):
+        x = torch.zeros(8, BIG[1], dtype=x_dtype)
+        x[torch.arange(8), k0 + torch.arange(8)] = -0.75
+        desc = m.descriptor(8, x_dtype=x_dtype, y_dtype=F32)
+        y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+        assert torch.equal(y.cpu().double(), -0.75 * W[:, k0:k0 + 8].T), k0
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
