@@ -650,6 +650,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             g4[i] = *reinterpret_cast<const float4*>(buf + block_at<4>(lane, i));
             u4[i] = *reinterpret_cast<const float4*>(buf + 2048 + block_at<4>(lane, i));
           }
+          // the reads above are done before the next block is written over them (__syncwarp
+          // alone orders no asynchronous copy: the block then arrived too early now and then)
+          fence_proxy_async();
           __syncwarp();
           if (c + 16 < COLS) fetch(m0, n0 + c + 16);
           else if (more) fetch(first_row(un), first_col(un));

@@ -509,7 +509,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             wb[i] = *reinterpret_cast<const uint32_t*>(sp + 1024 + at);
           }
         }
-        if (u == 1 || !two) {                        // the slot is read: bring the next one
+        // The slot is read (the fence: __syncwarp alone orders no asynchronous copy after the
+        // reads): bring the next one.
+        if (u == 1 || !two) {
+          fence_proxy_async();
           __syncwarp();
           if (++stage == p.depth) {
             stage = 0;

@@ -105,6 +105,31 @@ def test_backward_matches_64_bits(B, T, d, f, act, dtype):
         assert_norm_close(got[n], ref[n][0], dtype, n)
 
 
+def test_a_long_step_repeats_bit_for_bit(B):
+    """A step large enough to keep every SM busy (copies then arrive while others are still being
+    read), many times over: every result the same bits, and those of the reference."""
+    T, d, f = 2048, 1024, 8192
+    block, W = make(B, d, f)
+    x, dy = rows(T, d, BF), rows(T, d, BF, seed=2, scale=0.5)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc, backward=True)
+    names = ("y", "pre", "dx", "dw_gate", "dw_up", "dw_down")
+
+    def step():
+        pre = B.ffn_pre(desc)
+        y = B.ffn_forward(desc, x, ws, pre=pre)
+        return dict(zip(names, (y, pre, *B.ffn_backward(desc, x, dy, pre, ws))))
+    first = step()
+    for _ in range(40):
+        again = [step() for _ in range(3)][-1]
+        for n in names:
+            assert torch.equal(again[n], first[n]), n
+    ref = ffn_ref(x, *W, "silu", BF, dy=dy)
+    for n in ("y", "dx", "dw_gate", "dw_up", "dw_down"):
+        assert_close(first[n], *ref[n], BF, n)
+        assert_norm_close(first[n], ref[n][0], BF, n)
+
+
 def test_only_what_is_asked_for_is_computed(B):
     T, d, f = 200, 136, 264
     block, W = make(B, d, f)

@@ -205,6 +205,17 @@ def test_large_activations_overflow_only_where_the_result_does(B):
     assert (y == 0).all()
 
 
+@pytest.mark.parametrize("T,N,K,group", [(1, 65536, 2560, 128), (8, 30000, 4096, 64),
+                                         (16, 20000, 2560, 32), (32, 16384, 10240, 128)])
+def test_large_calls_repeat_bit_for_bit(B, T, N, K, group):
+    desc, x, W, b = make(B, T, N, K, group, y_dtype=F32)
+    ws, xd = B.alloc_matvec_workspace(desc), x.cuda()
+    first = B.matvec(desc, xd, ws)
+    for _ in range(100):
+        again = [B.matvec(desc, xd, ws) for _ in range(5)][-1]
+        assert torch.equal(again, first)
+
+
 @pytest.mark.parametrize("T,K", [(1, 2560), (32, 10240)])
 def test_captured_replayed_and_on_another_stream(B, T, K):
     """Two captured graphs with a workspace each, replayed at once on two streams."""
