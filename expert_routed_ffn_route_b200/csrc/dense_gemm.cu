@@ -30,8 +30,9 @@
 // the workspace and the epilogue warp that arrives last (a counter per warp) adds the parts in
 // order, so results do not depend on timing and no CTA waits for another.
 //
-// Roles (10 warps): warp 0 TMA, warp 1 TMEM and (leader) MMA, warps 2..9 epilogue (two warps a
-// TMEM lane quarter, each half of the columns). Every wait is bounded; one that gives up sets
+// Roles (11 warps): warps 0 and 10 TMA of A and of B (one thread for both needed 500 cycles a step,
+// the MMA 2 BN), warp 1 TMEM and (leader) MMA, warps 2..9 epilogue (two warps a TMEM lane
+// quarter, each half of the columns). Every wait is bounded; one that gives up sets
 // the status word and its site, and every role stops.
 #include <cstring>
 
@@ -44,7 +45,8 @@ namespace {
 
 constexpr int kBM = 128, kBK = 64;    // rows of one CTA, K values of a step
 constexpr int kPairM = 2 * kBM;
-constexpr int kGemmThreads = 320, kEpiWarps = 8;
+constexpr int kEpiWarps = 8, kWarpB = 2 + kEpiWarps;  // warp kWarpB: B's producer
+constexpr int kGemmThreads = 32 * (kWarpB + 1);
 constexpr int kMaxProblems = 4, kMaxPhases = 5;
 constexpr int kMaxPairs = 74;         // CTA pairs of a launch (148 SMs)
 constexpr int kGroupM = 16;           // row tiles walked together, for reuse in L2
@@ -219,11 +221,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 // Tile load into this CTA's shared memory, counted on the leader's barrier.
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1,
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                               uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
@@ -329,56 +331,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   Walk walk(pair);
   Unit u;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+  // The ring's stage and phase, counted along by the producers and the issuer.
+  struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++s == C::NS) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+  } ring;
+
+  if (warp == 0 || warp == kWarpB) {
+    // ------------------------------------------------------------ producers (both CTAs): A, B
     if (lane == 0) {
+      const bool is_a = warp == 0;
+      const uint32_t stage0 = smem_u32(smem) + (is_a ? 0 : C::A_BYTES);
+      const uint32_t full0 = leader_addr(&full[0]);
       int it = 0;
       bool ok = true;
       while (ok && !*abort_flag && walk.next(a, &u)) {
         const GemmProblem& q = a.p[u.p];
-        const int m0 = u.mt * kPairM + rank * kBM;
-        // this CTA's share of B: columns (rows of the weights) from n0 on; gate/up: all gate
-        // rows in the leader, all up rows in its peer
-        const int n0 = EPI == EPI_GATED ? u.nt * (BN / 2) : u.nt * BN + rank * (BN / 2);
-        for (int k = u.k0; k < u.k1; ++k, ++it) {
-          const int s = it % C::NS, use = it / C::NS;
-          if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1)) {
+        // first row (column) of this CTA's share; gate/up: all gate rows in the leader, all up
+        // rows in its peer
+        const int m0 = is_a                 ? u.mt * kPairM + rank * kBM
+                       : EPI == EPI_GATED   ? u.nt * (BN / 2)
+                                            : u.nt * BN + rank * (BN / 2);
+        const bool mn = is_a ? q.a_mn : EPI != EPI_GATED && q.b_mn;
+        const int boxes = mn ? (is_a ? kBM : BN / 2) / 64 : 1;
+        const int kt0 = q.kt[0];
+        for (int k = u.k0; k < u.k1; ++k, ++it, ring.next()) {
+          if (!mbar_wait(&empty[ring.s], ring.phase ^ 1)) {  // (a new barrier passes parity 1)
             ok = false;
             break;
           }
-          const int seg = k >= q.kt[0], kk = (seg ? k - q.kt[0] : k) * kBK;
-          uint8_t* as = smem + s * C::STAGE;
-          uint8_t* bs = as + C::A_BYTES;
-          const uint32_t bar = leader_addr(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
-          if (q.a_mn) {
-#pragma unroll
-            for (int i = 0; i < kBM / 64; ++i)
-              tma_load_pair(as + i * 8192, &q.a[seg], m0 + 64 * i, kk, bar);
+          const int seg = k >= kt0;
+          const int kk = (seg ? k - kt0 : k) * kBK;
+          const CUtensorMap* map = is_a ? &q.a[seg] : &q.b[EPI == EPI_GATED ? rank : seg];
+          const uint32_t dst = stage0 + ring.s * C::STAGE, bar = full0 + 8 * ring.s;
+          if (is_a && rank == 0) mbar_arrive_expect_tx(&full[ring.s], 2 * C::STAGE);
+          if (mn) {
+            tma_load_pair(dst, map, m0, kk, bar);
+            if (boxes > 1) tma_load_pair(dst + 8192, map, m0 + 64, kk, bar);
           } else {
-            tma_load_pair(as, &q.a[seg], kk, m0, bar);
-          }
-          if (EPI != EPI_GATED && q.b_mn) {
-#pragma unroll
-            for (int i = 0; i < BN / 128; ++i)
-              tma_load_pair(bs + i * 8192, &q.b[seg], n0 + 64 * i, kk, bar);
-          } else {
-            tma_load_pair(bs, &q.b[EPI == EPI_GATED ? rank : seg], kk, n0, bar);
+            tma_load_pair(dst, map, kk, m0, bar);
           }
         }
       }
       if (!ok) fail(50);
-      // every issued stage lands before the pair may exit (the leader waits for both shares)
-      if (rank == 0)
-        for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
-          mbar_wait(&full[j % C::NS], (j / C::NS) & 1);
+      // every issued stage lands before the pair may exit (the leader waits for all shares)
+      if (rank == 0 && is_a)
+        for (int j = 0; j < min(it, C::NS); ++j, ring.next()) {
+          // the last use of each stage, oldest first
+          const bool wrapped = it > C::NS;
+          const int s = wrapped ? ring.s : j;
+          mbar_wait(&full[s], wrapped ? ring.phase ^ 1 : 0);
+        }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
-      int it = 0, tile = 0;
+      int tile = 0;
       bool aborted = false;
+      const uint32_t stage0 = smem_u32(smem);
       for (; !aborted && walk.next(a, &u); ++tile) {
         const GemmProblem& q = a.p[u.p];
         // D fp32; A and B bf16 (1) or fp16 (0); majors; N; M
@@ -392,22 +409,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         tc_fence_after();
         const uint32_t dacc = tmem + b * BN;
         const uint64_t astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
-        for (int k = u.k0; k < u.k1; ++k, ++it) {
-          const int s = it % C::NS;
-          const bool ok = mbar_wait(&full[s], (it / C::NS) & 1);
+        // descriptors of stage 0; a stage is STAGE / 16 further on
+        const uint64_t ad0 = q.a_mn ? umma_desc_mn_sw128(stage0) : umma_desc_sw128(stage0);
+        const uint64_t bd0 = q.b_mn ? umma_desc_mn_sw128(stage0 + C::A_BYTES)
+                                    : umma_desc_sw128(stage0 + C::A_BYTES);
+        for (int k = u.k0; k < u.k1; ++k, ring.next()) {
+          const bool ok = mbar_wait(&full[ring.s], ring.phase);
           if (!__all_sync(0xffffffffu, ok)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t as = smem_u32(smem + s * C::STAGE), bs = as + C::A_BYTES;
-          const uint64_t ad = q.a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
-          const uint64_t bd = q.b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
+          const uint64_t off = (uint64_t)(ring.s * (C::STAGE >> 4));
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            umma_f16_pair(dacc, ad + kk * astep, bd + kk * bstep, idesc,
+            umma_f16_pair(dacc, ad0 + off + kk * astep, bd0 + off + kk * bstep, idesc,
                           (k > u.k0 || kk > 0) ? 1u : 0u);
-          umma_commit_pair(&empty[s]);
+          umma_commit_pair(&empty[ring.s]);
         }
         if (aborted) break;
         umma_commit_pair(&acc_full[b]);
@@ -779,10 +797,10 @@ bool block_map(CUtensorMap* m, const void* base, int rows, int cols, int ch, int
                                 : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
-// The schedule of a launch. Tile width and K splits by estimated cycles: a step of 16 K values
-// takes the MMA BN / 2 cycles and a CTA's share of the operands (128 + BN / 2) / 2 (64 bytes a
-// cycle from L2); a tile 1500 more to start and drain; a split tile's part 8 BN cycles to write
-// and each part as much again to read.
+// The schedule of a launch. Tile width and K splits by estimated cycles, from measured launches: an
+// SM takes in about 46 bytes a cycle (a step of 64 K values brings it (128 + BN / 2) * 128, more
+// than the MMA's 2 BN cycles allow for at every width), a tile takes 1500 more to start and
+// drain, and a split one 5000 for the fence and the count, 8 BN to write and 8 BN a part to read.
 struct GemmPlan {
   Phase ph[kMaxPhases];
   int n_phases, bn, units, slots, pairs;
@@ -790,13 +808,13 @@ struct GemmPlan {
   double cost;
 };
 
-double step_cycles(int bn) { return 4.0 * std::max(bn / 2, 64 + bn / 4); }
+double step_cycles(int bn) { return std::max(2.0 * bn, (128 + bn / 2) * 128 / 46.0); }
 
 // Cycles of `r` tiles of `steps` K steps on R idle pairs, split the best way.
 double split_cost(int r, int steps, int R, int bn, int* splits) {
   double best = -1;
   for (int s = 1; s <= std::min(std::min(R / r, steps), 16); ++s) {
-    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? (s + 1) * 8.0 * bn + 1000 : 0);
+    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? (s + 1) * 8.0 * bn + 5000 : 0);
     if (best < 0 || c < best) {
       best = c;
       *splits = s;
