@@ -122,26 +122,29 @@ struct Walk {
     }
     if (ph >= a.n_phases) return false;
     const Phase& f = a.ph[ph];
-    const int local = idx / f.splits;
-    const int t = f.first + local;
+    const unsigned local = f.splits == 1 ? idx : (unsigned)idx / (unsigned)f.splits;
+    const int t = f.first + (int)local;
     u->splits = f.splits;
-    u->part = idx - local * f.splits;
-    u->slot = f.slot + local;
+    u->part = idx - (int)local * f.splits;
+    u->slot = f.slot + (int)local;
     u->unit = f.unit + idx;
     u->p = 0;
 #pragma unroll
     for (int i = 1; i < kMaxProblems; ++i)
       if (i < a.n && t >= a.p[i].first) u->p = i;
     const GemmProblem& q = a.p[u->p];
-    const int l = t - q.first;
-    const int band = kGroupM * q.tiles_n;
-    const int b = l / band, r = l - b * band;
-    const int rows = min(kGroupM, q.tiles_m - b * kGroupM);
+    const unsigned l = t - q.first;
+    const unsigned b = l / (unsigned)(kGroupM * q.tiles_n), r = l - b * (kGroupM * q.tiles_n);
+    const unsigned rows = min(kGroupM, q.tiles_m - (int)b * kGroupM);
     u->nt = r / rows;
-    u->mt = b * kGroupM + r % rows;
+    u->mt = b * kGroupM + (r - u->nt * rows);
     const int steps = q.kt[0] + q.kt[1];
-    u->k0 = (int)((long long)steps * u->part / f.splits);
-    u->k1 = (int)((long long)steps * (u->part + 1) / f.splits);
+    u->k0 = 0;
+    u->k1 = steps;
+    if (f.splits > 1) {
+      u->k0 = (unsigned)(steps * u->part) / (unsigned)f.splits;
+      u->k1 = (unsigned)(steps * (u->part + 1)) / (unsigned)f.splits;
+    }
     return true;
   }
 };
