@@ -839,7 +839,9 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
     tiles[i] = (long long)((pr[i].M + kPairM - 1) / kPairM) * ((pr[i].N + cols - 1) / cols);
     g.order[i] = i;
   }
-  std::stable_sort(g.order, g.order + n, [&](int a, int b) { return steps[a] > steps[b]; });
+  for (int i = 1; i < n; ++i)  // longest first, equal ones in order
+    for (int j = i; j > 0 && steps[g.order[j]] > steps[g.order[j - 1]]; --j)
+      std::swap(g.order[j], g.order[j - 1]);
   // at most two lengths: the input gradient's and the weight gradients'
   long long count[2] = {0, 0};
   int len[2] = {steps[g.order[0]], 0};
