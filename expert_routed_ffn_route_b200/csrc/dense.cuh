@@ -10,6 +10,10 @@ namespace moe {
 
 constexpr int kMaxDevices = 64;      // per-device caches
 constexpr int kGemvMaxRows = 32;     // activation rows of the streaming kernels
+// Up to so many rows a streamed block passes h on as two 16-bit rows, the rounded value and the
+// rounded rest (together 16 bits or more): the down product has eight columns an instruction
+// anyway, so the second row costs nothing and y is rounded once.
+constexpr int kPairRows = 4;
 
 // Multiprocessors of the current device (0 on error), cached per device.
 int device_sms();
@@ -80,6 +84,11 @@ template <bool F16> __device__ __forceinline__ uint16_t round16(float v) {
   }
 }
 
+template <bool F16> __device__ __forceinline__ float value16(uint16_t b) {
+  if constexpr (F16) return __half2float(__ushort_as_half(b));
+  else return bf16_to_f32(b);
+}
+
 // ------------------------------------------------------------------ streaming kernels
 
 // One product of up to 32 activation rows with a weight matrix (dense_gemv.cu).
@@ -94,6 +103,8 @@ struct GemvArgs {
   int fmt, group;          // 4 (group 32, 64, 128) or 16
   bool f16, y32;           // activations (and 16-bit weights) fp16; output fp32
   int gated, act;          // y = act(w[0] x) * (w[1] x)
+  int pairs;               // rows 2 t and 2 t + 1 (of y if gated, else of x) are the rounded value
+                           // of token t and the rounded rest: see kPairRows
   float* partial;          // K parts: fp32 sums [tile][part][...]
   int32_t* counters;       // one per row tile, zero between calls
   int32_t* status;

@@ -128,6 +128,8 @@ GemvArgs ffn_gemv(const moe_ffn* F, int i) {
   a.f16 = b.fmt == MOE_W_FP16;
   a.gated = !i;
   a.act = F->act;
+  a.pairs = F->T <= kPairRows;
+  if (i && a.pairs) a.T = 2 * F->T;
   return a;
 }
 
@@ -156,7 +158,7 @@ FfnWs ffn_ws(const moe_ffn* F, bool backward) {
   w.partial_bytes = part;
   const size_t rows = align_up((size_t)F->T * F->f * 2);
   w.h = w.g.total;
-  w.dg = w.h + rows;
+  w.dg = w.h + (F->T <= kPairRows ? align_up((size_t)F->T * F->f * 4) : rows);
   w.du = w.dg + (backward ? rows : 0);
   w.total = w.du + (backward ? rows : 0);
   return w;

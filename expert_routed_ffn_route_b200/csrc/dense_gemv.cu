@@ -428,6 +428,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
 #pragma unroll
     for (int c = 0; c < TC; ++c) {
+      if (!GATED && TC == 1 && a.pairs) {  // columns 2 t4, 2 t4 + 1: the two rows of token t4
+        if (2 * t4 < a.T) {
+          uint8_t* to = static_cast<uint8_t*>(a.y) + (size_t)n * esize + t4 * col_bytes;
+          if (ok0) *reinterpret_cast<uint16_t*>(to) = round16<F16>(v[c][0] + v[c][1]);
+          if (ok1) *reinterpret_cast<uint16_t*>(to + 16) = round16<F16>(v[c][2] + v[c][3]);
+        }
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (c * 8 + 2 * t4 + j < a.T) {
@@ -435,7 +443,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           if constexpr (GATED) {
             const float act = a.act == MOE_ACT_SILU ? act_value<MOE_ACT_SILU>(v[c][j])
                                                     : act_value<MOE_ACT_GELU>(v[c][j]);
-            if (ok0) *reinterpret_cast<uint16_t*>(to) = round16<F16>(act * v[c][2 + j]);
+            const float h = act * v[c][2 + j];
+            const uint16_t r = round16<F16>(h);
+            if (TC == 1 && a.pairs) {
+              to = static_cast<uint8_t*>(a.y) + (size_t)n * 2 + 2 * (2 * t4 + j) * col_bytes;
+              // (an infinite value has no rest)
+              const float rest = h - value16<F16>(r);
+              if (ok0)
+                *reinterpret_cast<uint16_t*>(to + col_bytes) =
+                    round16<F16>(isfinite(rest) ? rest : 0.f);
+            }
+            if (ok0) *reinterpret_cast<uint16_t*>(to) = r;
           } else if (a.y32) {
             if (ok0) *reinterpret_cast<float*>(to) = v[c][j] + b0;
             if (ok1) *reinterpret_cast<float*>(to + 32) = v[c][2 + j] + b1;

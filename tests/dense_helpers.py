@@ -84,10 +84,12 @@ def additions(K):
     return K // 8 + 64
 
 
-def ffn_ref(x, wg, wu, wd, act, dtype, dy=None):
+def ffn_ref(x, wg, wu, wd, act, dtype, dy=None, h_half=None):
     """{name: (value in 64 bits, bound of a kernel's error before the result's own rounding)}:
-    fp32 sums, h, dg and du rounded to dtype, g and u kept in fp32."""
+    fp32 sums, h, dg and du rounded to dtype (h with half steps of h_half), g and u kept in
+    fp32."""
     half, tiny = HALF_STEP[dtype], TINY[dtype]
+    h_half = half if h_half is None else h_half
     x, wg, wu, wd = (t.double() for t in (x, wg, wu, wd))
     T, d = x.shape
     f = wg.shape[0]
@@ -99,7 +101,7 @@ def ffn_ref(x, wg, wu, wd, act, dtype, dy=None):
     h = a * u
     ea = ACT_LIPSCHITZ * eg + FUNC * (a.abs() + g.abs())
     eh = ea * u.abs() + a.abs() * eu + ea * eu
-    eh = eh + half * (h.abs() + eh) + tiny
+    eh = eh + h_half * (h.abs() + eh) + tiny
     out = {"y": (h @ wd.T, eh @ wd.abs().T + additions(f) * u32 * ((h.abs() + eh) @ wd.abs().T))}
     if dy is None:
         return out

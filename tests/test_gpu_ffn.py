@@ -196,6 +196,39 @@ def test_int4_block_matches_64_bits(B, T, d, f, act):
     assert (buf[T * d:] == 3).all()
 
 
+@pytest.mark.parametrize("fmt,dtype", [("int4", BF), (None, BF), (None, HF)])
+@pytest.mark.parametrize("T,d,f", [(1, 256, 256), (1, 2560, 1024), (3, 384, 2560), (4, 4096, 2560)])
+def test_few_rows_round_once(B, T, d, f, fmt, dtype):
+    """Up to four streamed rows carry h as its rounded value and the rounded rest (a half step of
+    a half step), so y is off by its own rounding and that."""
+    block, W = make(B, d, f, dtype, fmt=fmt, seed=T + d)
+    x = rows(T, d, dtype)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc)
+    half = torch.finfo(dtype).eps / 2
+    buf, y = guarded(T, d, dtype)
+    B.ffn_forward(desc, x, ws, out=y)
+    ref, bound = ffn_ref(x, *W, "silu", dtype, h_half=half * half)["y"]
+    assert_close(y, ref, bound, dtype, "y")
+    assert (buf[T * d:] == 3).all()
+    # one rounding of y, and fp32 sums: the 2-norm of the error is below one half step
+    assert ((y.double() - ref).norm() / ref.norm()).item() <= half
+
+
+def test_a_gate_beyond_fp16_gives_infinity_not_nan(B):
+    """h beyond fp16's largest value is infinite, with no rest, and so is y where Wd is not zero."""
+    d = f = 128
+    bank = dict(fmt="fp16", group=128, n_exp=1,
+                w_gate=torch.full((f, d), 30.0, dtype=HF, device="cuda"),
+                w_up=torch.full((f, d), 30.0, dtype=HF, device="cuda"),
+                w_down=torch.eye(d, dtype=HF, device="cuda") + 1)
+    block = B.DeviceFfn(bank, d, f)
+    for T in (1, 40):
+        desc = block.descriptor(T)
+        y = B.ffn_forward(desc, torch.ones(T, d, dtype=HF, device="cuda"), B.alloc_ffn_workspace(desc))
+        assert (y == float("inf")).all()
+
+
 def test_gates_far_from_zero(B):
     """Saturated gates: silu and gelu give g or 0 (never NaN), their slopes 1 or 0."""
     T, d, f = 64, 64, 64
