@@ -4,6 +4,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "pipeline.cuh"
 
 namespace moe {
@@ -19,7 +21,7 @@ constexpr int kPairRows = 4;
 int device_sms();
 // Opts a kernel into the largest dynamic shared memory on the current device, once per device;
 // `done` is the kernel's own array of kMaxDevices flags.
-cudaError_t allow_smem(const void* kernel, bool* done);
+cudaError_t allow_smem(const void* kernel, std::atomic<bool>* done);
 
 // Starts the fetch of a tensor map (a kernel's first TMA copy waits for its map otherwise).
 __device__ __forceinline__ void prefetch_map(const void* map) {

@@ -250,6 +250,7 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   gemv_scratch(a, &part, &cnt);
   const GemvWs w = gemv_ws(part, cnt);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
+  if (overlap(y, yb, ws, w.total)) return MOE_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.status = reinterpret_cast<int32_t*>(base);
   a.x = static_cast<const uint16_t*>(x);

@@ -735,7 +735,7 @@ template <int BN, int EPI, bool F16, int ACT>
 cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pdl) {
   using C = GemmCfg<BN, EPI>;
   auto kern = ffn_gemm_kernel<BN, EPI, F16, ACT>;
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices];
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg;

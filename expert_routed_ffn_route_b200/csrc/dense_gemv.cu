@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   // ---- the run
   bool ok = true;                                  // no wait has given up
-  uint32_t phase = 0;
-  int stage = 0, tile = tile0, slot = slot0;
+  uint32_t phase = 0, bad_phase = 0;
+  int stage = 0, bad_stage = 0, pending = 0, tile = tile0, slot = slot0;
   bool whole = slot0 == 0;                         // the tile's first slot is in this run
   float acc[TC][4], head[TC][4];
 #pragma unroll
@@ -503,9 +503,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
       load_scales();
       const uint8_t* sp = ring + stage * kSlotBytes;
-      if (ok && !mbar_wait(&full[stage], phase)) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
         set_timeout(a.status, kSiteGemvSlot);
-        ok = false;
+        ok = false;                                // no more copies; those on the way are waited
+        pending = n_my - cleft - it;               // for below
+        bad_stage = stage;
+        bad_phase = phase;
+        cleft = 0;
       }
       const bool two = 2 * slot + 1 < n_units;
 #pragma unroll
@@ -627,6 +631,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (MASKED && masked) run(std::integral_constant<bool, MASKED>{});
   else run(std::false_type{});
 
+  // after a timeout: the copies still on the way land (or their waits give up) before the ring is
+  // written or the CTA ends
+  for (; pending > 0; --pending) {
+    mbar_wait(&full[bad_stage], bad_phase);
+    if (++bad_stage == p.depth) {
+      bad_stage = 0;
+      bad_phase ^= 1;
+    }
+  }
+
   // ---- tiles that several warps share: each leaves the sums of the tile it did not begin
   // ("head") in its ring, which nothing is on its way into any more; the warp that began a tile
   // adds the heads after it to its own, in warp order
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 template <int FMT, int GROUP, bool F16, int TC, bool GATED, bool MASKED = false>
 cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
   auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED, MASKED>;
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices];
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
   if (err != cudaSuccess) return err;
   GemvMaps maps;
@@ -756,18 +770,18 @@ cudaError_t launch_fmt(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bo
 }  // namespace
 
 int device_sms() {
-  static int sms[kMaxDevices] = {};
+  static std::atomic<int> sms[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (sms[dev] == 0) {  // racing threads store the same value
-    int n = 0;
+  int n = sms[dev];
+  if (n == 0) {  // racing threads store the same value
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     sms[dev] = n;
   }
-  return sms[dev];
+  return n;
 }
 
-cudaError_t allow_smem(const void* kernel, bool* done) {
+cudaError_t allow_smem(const void* kernel, std::atomic<bool>* done) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;

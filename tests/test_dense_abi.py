@@ -58,6 +58,7 @@ def test_matvec_rejects_bad_arguments_before_any_cuda_call(lib):
     assert call(FAKE, FAKE + 64, FAKE, 1 << 30) == -1      # y over x
     assert call(FAKE, m.w + 64, FAKE, 1 << 30) == -1       # y over the codes
     assert call(FAKE, m.s + 64, FAKE, 1 << 30) == -1       # y over the scales
+    assert call(FAKE, far, far, 1 << 30) == -1             # y over the workspace
     assert lib.moe_matvec(None, FAKE, far, FAKE, 1 << 30, None) == -1
 
 

@@ -196,6 +196,22 @@ def test_int4_block_matches_64_bits(B, T, d, f, act):
     assert (buf[T * d:] == 3).all()
 
 
+@pytest.mark.parametrize("T,d,f,fmt", [(32, 32768, 136, None), (3, 136, 32768, None),
+                                       (32, 32768, 128, "int4"), (40, 32768, 72, None)])
+def test_the_longest_rows(B, T, d, f, fmt):
+    """The widest blocks: rows that are split into K parts, in both products."""
+    block, W = make(B, d, f, fmt=fmt, seed=d)
+    x = rows(T, d, BF)
+    desc = block.descriptor(T)
+    ws = B.alloc_ffn_workspace(desc)
+    y = B.ffn_forward(desc, x, ws)
+    assert torch.equal(y, B.ffn_forward(desc, x, ws))
+    ref, bound = ffn_ref(x, *W, "silu", BF)["y"]
+    assert_close(y, ref, bound, BF, "y")
+    assert_norm_close(y, ref, BF, "y")
+    assert B.ffn_device_status(desc, ws) == (0, 0)
+
+
 @pytest.mark.parametrize("fmt,dtype", [("int4", BF), (None, BF), (None, HF)])
 @pytest.mark.parametrize("T,d,f", [(1, 256, 256), (1, 2560, 1024), (3, 384, 2560), (4, 4096, 2560)])
 def test_few_rows_round_once(B, T, d, f, fmt, dtype):
