@@ -513,14 +513,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                                  __uint_as_float(r[i][4 * j + 2]),
                                  __uint_as_float(r[i][4 * j + 3])));
         }
-        __threadfence();
+        fence_acq_rel_gpu();
         __syncwarp();
         int last = 0;
         if (lane == 0) {
           int32_t* cnt = a.counters + ((size_t)u.slot * 2 + rank) * kEpiWarps + (warp - 2);
           last = atomicAdd(cnt, 1) == u.splits - 1;
           if (last) *cnt = 0;
-          __threadfence();
+          fence_acq_rel_gpu();
         }
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();

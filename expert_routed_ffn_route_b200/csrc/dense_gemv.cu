@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   // the tiles whose last part this was.
   if (p.parts > 1) {
     const int from = tile0 + (slot0 != 0), to = tile + (open && whole);
-    __threadfence();
+    fence_acq_rel_gpu();
     __syncwarp();
     for (int t0 = from; t0 < to; t0 += 32) {
       bool last = false;
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (last) a.counters[t0 + lane] = 0;
       }
       uint32_t mask = __ballot_sync(0xffffffffu, last);
-      if (mask) __threadfence();
+      if (mask) fence_acq_rel_gpu();
       while (mask) {
         const int t = t0 + __ffs(mask) - 1;
         mask &= mask - 1;
