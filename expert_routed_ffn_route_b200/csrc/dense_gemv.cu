@@ -49,6 +49,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kSlotBytes = 2048;                 // 16 rows x 128 bytes
 constexpr int kRingSlot = kWarps * kSlotBytes;   // one slot of every warp's ring
 constexpr int kMaxDepth = 6;
+constexpr int kSms = 148;
 constexpr int kSiteGemvSlot = 60;
 // The masked form from so many 16-row x 128-code units on. Its sums and its look at the rows cost
 // a call 0.3 us: 1024 x 2560 (1280 units) 4.5 us against 4.2, 10240 x 2560 (12800) 8.8 against
@@ -92,9 +93,28 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   const int unit_bytes = p.unit_k * 2 * p.cols + p.sums;
   const int room = kSmemMax - 2048;                // beside the staged rows: two slots a warp
   const int fit = std::max(2, (room - 2 * kRingSlot) / unit_bytes & ~1);
-  p.parts = (p.units + fit - 1) / fit;
-  p.part_units = ((p.units + p.parts - 1) / p.parts + 1) & ~1;
-  p.parts = (p.units + p.part_units - 1) / p.part_units;
+  // K parts: at least so many that a part's rows fit; more where that is estimated shorter (cycles
+  // of a CTA, from measured calls): its rows come in at 20 bytes a cycle while every SM fetches
+  // the same ones, its slots go through 16 warps, and with parts the sums go through the
+  // workspace. 16 rows on 2560 x 10240, groups of 32: 17.0 us in two parts, 13.7 in seven; 32 rows
+  // on 10240 x 2560: 15.5 in one, 15.1 in two, 17.1 in three. (The SM count is the B200's here: the
+  // workspace's size follows from it.)
+  const int fewest = (p.units + fit - 1) / fit;
+  double best = -1;
+  for (int parts = fewest; parts <= std::max(fewest, 8); ++parts) {
+    const int part_units = ((p.units + parts - 1) / parts + 1) & ~1;
+    const int real = (p.units + part_units - 1) / part_units;
+    const int groups = std::min(std::max(1, kSms / real), p.tiles);
+    const double unit = a.fmt == 16 ? 250 : p.tc == 1 ? 1000 : p.tc == 2 ? 1100 : 1500;
+    double cost = (double)part_units * unit_bytes / 20 +
+                  (double)((p.tiles + groups - 1) / groups) * part_units / kWarps * unit;
+    if (real > 1) cost += 2500 + (double)real * p.tiles * p.tc * 1024 / kSms / 20;
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.parts = real;
+      p.part_units = part_units;
+    }
+  }
   const int xbytes = p.part_units * unit_bytes;
   p.depth = std::min(kMaxDepth, (room - xbytes) / kRingSlot);
   p.groups = std::min(std::max(1, sms / p.parts), p.tiles);
