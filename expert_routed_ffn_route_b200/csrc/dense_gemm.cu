@@ -17,10 +17,10 @@
 // rows of A and half of B's columns by TMA, the leader's MMA warp issues tcgen05.mma kind::f16
 // (M = 256, N = BN) over both, and each CTA's TMEM receives its 128 rows, in one of two
 // accumulators while the epilogue warps empty the other. Why pairs: an SM takes in about 47
-// bytes a cycle from L2 (measured at every tile width), a 128 x 256 tile of one CTA would need 96
+// bytes a cycle from L2 (measured at every tile width, at full clock), a 128 x 256 tile of one CTA would need 96
 // at the MMA's full rate (it reached 967 TFLOP/s on a 4096 x 2560 x 10240 forward pass), a pair's
-// 256 x 256 tile needs 64: the intake still binds, at 73 % of the tensor peak, which is where the
-// measured library GEMM is too.
+// 256 x 256 tile needs 64: at full clock the intake binds at 73 % of the tensor peak, where the
+// measured library GEMM is too; under the power cap (1.6 GHz) the tensor pipe is 83 % busy.
 // An operand is read as it lies in memory: with K contiguous (x, dy, h, dg, du and the forward
 // weights) or with K as the slow dimension (the weights of dh and dx, and both operands of the
 // weight gradients), as the MMA's "K-major" or "MN-major" operand; no transposed copies are
@@ -43,8 +43,8 @@
 // the status word and its site, and every role stops.
 //
 // Measured on one B200 (kernel time in graphs / in a steady loop under the power cap): forward of
-// 4096 rows, 2560 x 10240, 428 / 490 us (1505 / 1315 TFLOP/s; 1631 and 1375 are the measured
-// library peaks), training step 1.40 / 1.59 ms (1380 / 1216).
+// 4096 rows, 2560 x 10240, 410 / 495 us (1573 / 1300 TFLOP/s; 1631 and 1375 are the measured
+// library peaks), training step 1.36..1.50 / 1.59..1.66 ms (1420 / 1216).
 #include <cstring>
 
 #include "dense.cuh"
@@ -503,7 +503,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       // A part of a split tile: this warp's sums into the workspace, 16 bytes a lane and row of
       // 512 bytes; the warp that brings the last part goes on with the sum of all.
       const float4* parts = nullptr;
-      if (u.splits > 1) {
+      auto hand_back = [&]() {  // the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
+      };
+      bool mine = m0 < q.M && n0 < q.N;  // (rows or columns past the edges: nothing to do)
+      if (!mine) {
+        hand_back();
+      } else if (u.splits > 1) {
         const size_t unit_f4 = (size_t)2 * kEpiWarps * (ACC / 4) * 32;
         const size_t my = ((size_t)rank * kEpiWarps + (warp - 2)) * (ACC / 4) * 32 + lane;
         float4* base = reinterpret_cast<float4*>(a.partial);
@@ -536,21 +544,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();
         parts = base + (size_t)(u.unit - u.part) * unit_f4 + my;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
-        if (!last) {
-          if (EPI == EPI_GRAD && more) {  // the block in the buffer is not this warp's to finish
-            if (!mbar_wait(in_bar, in_phase)) {
-              fail(53);
-              break;
-            }
-            in_phase ^= 1;
-            __syncwarp();
-            fetch(first_row(un), first_col(un));
+        hand_back();
+        mine = last;
+      }
+      if (!mine) {
+        if (EPI == EPI_GRAD && more) {  // the block in the buffer is not this warp's to finish
+          if (!__all_sync(0xffffffffu, mbar_wait(in_bar, in_phase))) {
+            fail(53);
+            break;
           }
-          continue;
+          in_phase ^= 1;
+          fetch(first_row(un), first_col(un));
         }
+        continue;
       }
       // NC chunks of 16 accumulator columns from chunk column c on: from TMEM, or the sum of the
       // parts (all loads of a part in flight at once)
@@ -587,10 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       };
       // the accumulator is free once its last columns are read (a split tile's already is)
       auto release = [&]() {
-        if (parts) return;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty_leader[b]);
+        if (!parts) hand_back();
       };
       // The buffer's previous block has been read; then, after this lane's part is written, the
       // block may be stored.
@@ -824,11 +827,12 @@ struct GemmPlan {
 
 double step_cycles(int bn) { return std::max(2.0 * bn, (128 + bn / 2) * 128 / 46.0); }
 
-// Cycles of `r` tiles of `steps` K steps on R idle pairs, split the best way.
-double split_cost(int r, int steps, int R, int bn, int* splits) {
+// Cycles of `r` tiles of `steps` K steps on R idle pairs, split the best way; `used`: the share of
+// the tiles' area that holds results (the rest is not exchanged).
+double split_cost(int r, int steps, int R, int bn, double used, int* splits) {
   double best = -1;
   for (int s = 1; s <= std::min(std::min(R / r, steps), 16); ++s) {
-    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? (s + 1) * 8.0 * bn + 5000 : 0);
+    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? 6000 + (8 * used + 5.5 * s) * bn : 0);
     if (best < 0 || c < best) {
       best = c;
       *splits = s;
@@ -844,8 +848,8 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
   g.pairs = R;
   int steps[kMaxProblems];
   long long tiles[kMaxProblems];
+  const int cols = gated ? bn / 2 : bn;
   for (int i = 0; i < n; ++i) {
-    const int cols = gated ? bn / 2 : bn;
     steps[i] = (pr[i].K[0] + kBK - 1) / kBK + (pr[i].K[1] + kBK - 1) / kBK;
     tiles[i] = (long long)((pr[i].M + kPairM - 1) / kPairM) * ((pr[i].N + cols - 1) / cols);
     g.order[i] = i;
@@ -855,13 +859,16 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
       std::swap(g.order[j], g.order[j - 1]);
   // at most two lengths: the input gradient's and the weight gradients'
   long long count[2] = {0, 0};
+  double area[2] = {0, 0};
   int len[2] = {steps[g.order[0]], 0};
   for (int i = 0; i < n; ++i) {
     const int o = g.order[i];
     const int c = steps[o] == len[0] ? 0 : 1;
     if (c) len[1] = steps[o];
     count[c] += tiles[o];
+    area[c] += (double)pr[o].M * pr[o].N;
   }
+  const double count0 = count[0], count1 = count[1];
   const auto whole = [&](int c) { return len[c] * step_cycles(bn) + 1500; };
   int first = 0;
   const auto add = [&](long long cnt, int splits, int lo, int np) {
@@ -898,7 +905,7 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
   }
   if (e) {
     int s = 1;
-    g.cost += split_cost(e, len[0], R, bn, &s);
+    g.cost += split_cost(e, len[0], R, bn, area[0] / (count0 * 256.0 * cols), &s);
     add(e, s, 0, e * s);
   }
   if (count[1] > 0) {
@@ -908,7 +915,7 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
     g.cost += full / R * whole(1);
     if (e) {
       int s = 1;
-      g.cost += split_cost(e, len[1], R, bn, &s);
+      g.cost += split_cost(e, len[1], R, bn, area[1] / (count1 * 256.0 * cols), &s);
       add(e, s, 0, e * s);
     }
   }
