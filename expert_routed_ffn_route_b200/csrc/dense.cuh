@@ -139,13 +139,16 @@ struct FfnArgs {
   int32_t* status;
   float* partial;      // sums of tiles split along K
   size_t partial_bytes;
-  int32_t* counters;   // ffn_counters() of them, zero between calls
+  int32_t* counters;   // kFfnCounters of them, zero between calls
 };
 
+// A launch cuts the leftover tiles of at most two rounds of 74 CTA pairs; a counter for each of the
+// 16 epilogue warps of a pair.
+constexpr size_t kFfnCounters = 2 * 74 * 16;
+
 // Workspace of the tensor-core kernels, whatever the sizes: bytes of partial sums (a forward
-// launch splits one leftover round of tiles, a backward launch at most two), number of counters.
+// launch splits one leftover round of tiles, a backward launch at most two).
 size_t ffn_partial_bytes(bool backward);
-size_t ffn_counters();
 
 cudaError_t launch_ffn_gate_up(const FfnArgs& a, cudaStream_t st);          // x -> h (and pre)
 cudaError_t launch_ffn_down(const FfnArgs& a, cudaStream_t st);             // h -> y

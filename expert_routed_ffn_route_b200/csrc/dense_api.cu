@@ -60,22 +60,37 @@ GemvArgs matvec_args(const moe_matrix* M) {
   return a;
 }
 
-// Workspace of one or two streaming products: a first block of 256 bytes (status words of the
-// tensor-core kernels), the row tiles' counters, the partial sums.
+// A workspace begins with a block of status words and kWsCounters counters, in the same place for
+// every call, so that calls of any matrices and blocks can use one workspace in turn: what one
+// leaves there (partial sums, h) never lies where the next expects its counters at zero. Then come
+// the partial sums. A split product of more row tiles than that (over 131072 outputs) has its
+// counters behind the others and clears them itself, before its kernel.
+constexpr size_t kWsCounters = 8192;
+
 struct GemvWs {
   size_t counters, partial, total;
+  bool clear;
 };
 GemvWs gemv_ws(size_t partial_bytes, size_t n_counters) {
   GemvWs w;
-  w.counters = kAlign;
-  w.partial = align_up(w.counters + 4 * n_counters);
+  const size_t fixed = kAlign + 4 * kWsCounters;
+  w.clear = n_counters > kWsCounters;
+  w.counters = w.clear ? fixed : kAlign;
+  w.partial = w.clear ? align_up(fixed + 4 * n_counters) : fixed;
   w.total = align_up(w.partial + partial_bytes);
+  return w;
+}
+// A product that is not split uses the status words alone.
+GemvWs matvec_ws(size_t partial_bytes, size_t n_counters) {
+  GemvWs w = gemv_ws(partial_bytes, n_counters);
+  if (n_counters == 0) w.total = kAlign;
   return w;
 }
 
 // ------------------------------------------------------------------ dense gated block
 
 constexpr int kMaxWidth = 32768, kMaxFfnRows = 1 << 20;
+static_assert(kMaxWidth / 8 <= kWsCounters && kFfnCounters <= kWsCounters, "counters");
 
 inline bool is_16bit(const moe_ffn* F) {
   return F->bank.fmt == MOE_W_BF16 || F->bank.fmt == MOE_W_FP16;
@@ -134,28 +149,25 @@ GemvArgs ffn_gemv(const moe_ffn* F, int i) {
   return a;
 }
 
-// Workspace of a block: the status block, counters and partial sums (of the streaming kernels or
-// the tensor-core kernels; a call's products run one after the other and share them), h, and
-// for the backward pass dg, du.
+// Workspace of a block: the status words, the counters (at most 4096, see kMaxWidth) and partial
+// sums of the streaming kernels or the tensor-core kernels (a call's products run one after the
+// other and share them), h, and for the backward pass dg, du.
 struct FfnWs {
   GemvWs g;
   size_t partial_bytes, h, dg, du, total;
 };
 FfnWs ffn_ws(const moe_ffn* F, bool backward) {
   FfnWs w;
-  size_t part = 0, cnt = 0;
+  size_t part = 0;
   if (F->T <= kGemvMaxRows)
     for (int i = 0; i < 2; ++i) {
       size_t p, c;
       gemv_scratch(ffn_gemv(F, i), &p, &c);
       part = std::max(part, p);
-      cnt = std::max(cnt, c);
     }
-  if (is_16bit(F) && (backward || F->T > kGemvMaxRows)) {
+  if (is_16bit(F) && (backward || F->T > kGemvMaxRows))
     part = std::max(part, ffn_partial_bytes(backward));
-    cnt = std::max(cnt, ffn_counters());
-  }
-  w.g = gemv_ws(part, cnt);
+  w.g = gemv_ws(part, kWsCounters);
   w.partial_bytes = part;
   const size_t rows = align_up((size_t)F->T * F->f * 2);
   w.h = w.g.total;
@@ -233,7 +245,7 @@ size_t moe_matvec_workspace_size(const moe_matrix* M) {
   if (matvec_validate(M) != MOE_OK) return 0;
   size_t part, cnt;
   gemv_scratch(matvec_args(M), &part, &cnt);
-  return gemv_ws(part, cnt).total;
+  return matvec_ws(part, cnt).total;
 }
 
 moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, size_t ws_bytes,
@@ -249,7 +261,7 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   GemvArgs a = matvec_args(M);
   size_t part, cnt;
   gemv_scratch(a, &part, &cnt);
-  const GemvWs w = gemv_ws(part, cnt);
+  const GemvWs w = matvec_ws(part, cnt);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
   if (overlap(y, yb, ws, w.total)) return MOE_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -258,7 +270,9 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   a.y = y;
   a.counters = reinterpret_cast<int32_t*>(base + w.counters);
   a.partial = reinterpret_cast<float*>(base + w.partial);
-  MOE_TRY(launch_gemv_rows(a, reinterpret_cast<cudaStream_t>(stream), false));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (w.clear) MOE_TRY(cudaMemsetAsync(a.counters, 0, 4 * cnt, st));
+  MOE_TRY(launch_gemv_rows(a, st, false));
   return MOE_OK;
 }
 

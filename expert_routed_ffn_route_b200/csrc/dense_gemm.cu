@@ -62,6 +62,7 @@ constexpr int kMaxProblems = 4, kMaxPhases = 5;
 constexpr int kMaxPairs = 74;         // CTA pairs of a launch (148 SMs)
 constexpr int kGroupM = 16;           // row tiles walked together, for reuse in L2
 constexpr int kSmemBytes = 227 * 1024;
+static_assert(kFfnCounters == 2 * kMaxPairs * 2 * kEpiWarps, "a counter a warp of every cut tile");
 
 enum Epi { EPI_STORE = 0, EPI_GATED = 1, EPI_GRAD = 2 };
 
@@ -1038,8 +1039,6 @@ Product down_product(const FfnArgs& f) {
 size_t ffn_partial_bytes(bool backward) {
   return (size_t)(backward ? 2 : 1) * kMaxPairs * kPairM * 256 * sizeof(float);
 }
-
-size_t ffn_counters() { return (size_t)2 * kMaxPairs * 2 * kEpiWarps; }
 
 cudaError_t launch_ffn_gate_up(const FfnArgs& f, cudaStream_t st) {
   const Product p = gate_up_product(f);

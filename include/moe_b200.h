@@ -325,11 +325,13 @@ MOE_API moe_status moe_matvec_validate(const moe_matrix* M);
 
 /* Bytes of device workspace of a call (0 if M is invalid; at least 256): as for the layer,
  * caller-owned, 256-byte aligned, zeroed once before its first use (and again after a call that
- * reported MOE_ERR_TIMEOUT), reusable by calls ordered on one stream and not shared by calls
- * that can overlap (two captured graphs that replay at once need one each). */
+ * reported MOE_ERR_TIMEOUT), reusable by calls ordered on one stream, moe_matvec of any matrices and
+ * the moe_ffn calls of any blocks, if it is large enough for each; not shared by calls that can
+ * overlap (two captured graphs that replay at once need one each) or with a layer's calls. */
 MOE_API size_t moe_matvec_workspace_size(const moe_matrix* M);
 
-/* y = x W^T (+ bias), one kernel. x [T][ldx], y [T][ldy]. */
+/* y = x W^T (+ bias), one kernel (above 131072 outputs with K split, a clear of its counters before
+ * it). x [T][ldx], y [T][ldy]. */
 MOE_API moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws,
                               size_t ws_bytes, moe_stream_t stream);
 

@@ -105,6 +105,38 @@ def test_backward_matches_64_bits(B, T, d, f, act, dtype):
         assert_norm_close(got[n], ref[n][0], dtype, n)
 
 
+def test_calls_of_any_kind_share_one_workspace_in_turn(B):
+    """Streamed and tensor-core calls, forward and backward, of blocks and matrices of several
+    sizes use one workspace one after the other; every result has the bits that a workspace of its
+    own gives (what one call leaves behind is nothing that another counts on)."""
+    gen = torch.Generator().manual_seed(5)
+    calls = []
+    for T, d, f in ((1, 2560, 1024), (16, 1024, 2056), (32, 2560, 1024), (40, 512, 1032), (4, 72, 4096)):
+        block, _ = make(B, d, f, seed=T)
+        desc, x, dy = block.descriptor(T), rows(T, d, BF, T), rows(T, d, BF, T + 1)
+
+        def train(ws, desc=desc, x=x, dy=dy):
+            pre = B.ffn_pre(desc)
+            y = B.ffn_forward(desc, x, ws, pre=pre)
+            return (y, *B.ffn_backward(desc, x, dy, pre, ws))
+        calls.append((lambda ws, desc=desc, x=x: (B.ffn_forward(desc, x, ws),),
+                      B.alloc_ffn_workspace(desc)))
+        calls.append((train, B.alloc_ffn_workspace(desc, backward=True)))
+    for T, N, K in ((32, 1000, 10240), (16, 2560, 10240), (1, 77, 256)):
+        codes, scales = quantise(gen, N, K, 32)
+        desc = B.QuantMatrix(codes.cuda(), scales.cuda(), K, 32).descriptor(T)
+        calls.append((lambda ws, desc=desc, x=rows(T, K, BF, N): (B.matvec(desc, x, ws),),
+                      B.alloc_matvec_workspace(desc)))
+    own = [fn(ws) for fn, ws in calls]
+    shared = torch.zeros(max(ws.numel() for _, ws in calls), dtype=torch.uint8, device="cuda")
+    n = len(calls)
+    for i in range(n):
+        for j in range(n):                         # each call after each other one
+            for k in (i, j):
+                got = calls[k][0](shared)
+                assert all(torch.equal(a, b) for a, b in zip(got, own[k])), (i, j, k)
+
+
 def test_a_long_step_repeats_bit_for_bit(B):
     """A step large enough to keep every SM busy (copies then arrive while others are still being
     read), many times over: every result the same bits, and those of the reference."""

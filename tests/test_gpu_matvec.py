@@ -58,6 +58,27 @@ def test_matches_64_bits(B, T, N, K, group, x_dtype, y_dtype):
     check(y, x, W, b, group, f"{T}x{N}x{K} g{group}")
 
 
+def test_many_outputs_with_k_in_parts(B):
+    """More row tiles than a workspace has fixed counters for, K split: the call clears its own,
+    whatever the workspace held there."""
+    T, N, K = 32, 131120, 4096
+    gen = torch.Generator().manual_seed(8)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=gen).to(torch.int32)
+    scales = (torch.rand(N, K // 128, generator=gen) * 2.0 ** -8 + 2.0 ** -9).to(BF)
+    x = torch.randn(T, K, generator=gen).to(BF)
+    m = B.QuantMatrix(codes.cuda(), scales.cuda(), K)
+    desc = m.descriptor(T, y_dtype=F32)
+    ws = B.alloc_matvec_workspace(desc)
+    assert ws.numel() > 256 + 4 * 8192 + 4 * (N // 16)      # split
+    y = B.matvec(desc, x.cuda(), ws)
+    ws[256 + 4 * 8192:] = 255
+    assert torch.equal(y, B.matvec(desc, x.cuda(), ws))
+    assert torch.equal(y, B.matvec(desc, x.cuda(), ws))
+    for at in (0, N // 2, N - 3000):                        # three stretches against 64 bits
+        rows = slice(at, at + 3000)
+        check(y[:, rows], x, dequantise(codes[rows], scales[rows], 128), None, 128, at)
+
+
 # ---- calls large enough for the products on shifted codes (few rows, groups of 128): the sums
 # are sum((q + 8) x) - 8 sum(x), so their terms' magnitudes are those of |q| + 8
 
