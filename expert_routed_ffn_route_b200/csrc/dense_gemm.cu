@@ -480,18 +480,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     Unit un;
     bool more = walk.next(a, &un);
     if (EPI == EPI_GRAD && more) fetch(first_row(un), first_col(un));
-    for (; !*abort_flag && more; ++tile) {
+    // (whole warps go on or stop: the TMEM loads are warp-wide)
+    for (; more && !__any_sync(0xffffffffu, *abort_flag); ++tile) {
       u = un;
       more = walk.next(a, &un);
       const GemmProblem& q = a.p[u.p];
       const int b = tile & 1;
       const int m0 = first_row(u), n0 = first_col(u);
-      if (!mbar_wait(&acc_full[b], (tile >> 1) & 1)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (tile >> 1) & 1))) {
         fail(52);
         break;
       }
       tc_fence_after();
-      __syncwarp();
       const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * COLS;
       // Accumulator column i (0..15) of chunk c of this warp: gate/up chunks are 16 gate columns,
       // then 16 up columns.
