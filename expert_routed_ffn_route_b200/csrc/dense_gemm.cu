@@ -43,8 +43,8 @@
 // the status word and its site, and every role stops.
 //
 // Measured on one B200 (kernel time in graphs / in a steady loop under the power cap): forward of
-// 4096 rows, 2560 x 10240, 410 / 495 us (1573 / 1300 TFLOP/s; 1631 and 1375 are the measured
-// library peaks), training step 1.36..1.50 / 1.59..1.66 ms (1420 / 1216).
+// 4096 rows, 2560 x 10240, 426 / 495 us (1514 / 1300 TFLOP/s; 1631 and 1375 are the measured
+// library peaks), training step 1.41 / 1.59..1.66 ms (1371 / 1190).
 #include <cstring>
 
 #include "dense.cuh"
@@ -828,18 +828,24 @@ struct GemmPlan {
 
 double step_cycles(int bn) { return std::max(2.0 * bn, (128 + bn / 2) * 128 / 46.0); }
 
-// Cycles of `r` tiles of `steps` K steps on R idle pairs, split the best way; `used`: the share of
-// the tiles' area that holds results (the rest is not exchanged).
+// Cycles of a tile of `steps` K steps in s parts; `used`: the share of the tile's area that holds
+// results (the rest is not exchanged).
+double tile_cycles(int steps, int s, int bn, double used) {
+  return (steps + s - 1) / s * step_cycles(bn) + 1500 +
+         (s > 1 ? 6000 + (8 * used + 5.5 * s) * bn : 0);
+}
+
+// Cycles of `r` tiles on R idle pairs, split the best way.
 double split_cost(int r, int steps, int R, int bn, double used, int* splits) {
   double best = -1;
   for (int s = 1; s <= std::min(std::min(R / r, steps), 16); ++s) {
-    const double c = (steps + s - 1) / s * step_cycles(bn) + (s > 1 ? 6000 + (8 * used + 5.5 * s) * bn : 0);
+    const double c = tile_cycles(steps, s, bn, used);
     if (best < 0 || c < best) {
       best = c;
       *splits = s;
     }
   }
-  return best + 1500;
+  return best;
 }
 
 GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
@@ -869,8 +875,8 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
     count[c] += tiles[o];
     area[c] += (double)pr[o].M * pr[o].N;
   }
-  const double count0 = count[0], count1 = count[1];
-  const auto whole = [&](int c) { return len[c] * step_cycles(bn) + 1500; };
+  double used[2];
+  for (int c = 0; c < 2; ++c) used[c] = count[c] ? area[c] / (count[c] * 256.0 * cols) : 1;
   int first = 0;
   const auto add = [&](long long cnt, int splits, int lo, int np) {
     if (cnt <= 0) return;
@@ -888,38 +894,58 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
     }
     first += (int)cnt;
   };
-  long long full = count[0] / R * R;
-  int e = (int)(count[0] - full);
-  add(full, 1, 0, R);
-  g.cost = full / R * whole(0);
-  if (e && count[1] > 0) {
-    // the leftover long tiles beside as many rounds of short ones on the other pairs, if there
-    // are that many; else split over all pairs
-    const int x = (len[0] + len[1] / 2) / len[1];
-    if ((long long)x * (R - e) <= count[1]) {
-      add(e, 1, 0, e);
-      add((long long)x * (R - e), 1, e, R - e);
-      count[1] -= (long long)x * (R - e);
-      g.cost += whole(0);
-      e = 0;
-    }
-  }
-  if (e) {
+  // cnt tiles of length c over all pairs: whole rounds, then the rest split
+  const auto rounds_cost = [&](long long cnt, int c, int* s) {
+    const int rest = (int)(cnt % R);
+    return cnt / R * tile_cycles(len[c], 1, bn, 1) +
+           (rest ? split_cost(rest, len[c], R, bn, used[c], s) : 0);
+  };
+  const auto rounds = [&](long long cnt, int c) {
     int s = 1;
-    g.cost += split_cost(e, len[0], R, bn, area[0] / (count0 * 256.0 * cols), &s);
-    add(e, s, 0, e * s);
+    g.cost += rounds_cost(cnt, c, &s);
+    const long long rest = cnt % R;
+    add(cnt - rest, 1, 0, R);
+    add(rest, s, 0, (int)rest * s);
+  };
+  const int e = (int)(count[0] % R);
+  if (!e || !count[1]) {
+    rounds(count[0], 0);
+    if (count[1]) rounds(count[1], 1);
+    return g;
   }
-  if (count[1] > 0) {
-    full = count[1] / R * R;
-    e = (int)(count[1] - full);
-    add(full, 1, 0, R);
-    g.cost += full / R * whole(1);
-    if (e) {
-      int s = 1;
-      g.cost += split_cost(e, len[1], R, bn, area[1] / (count1 * 256.0 * cols), &s);
-      add(e, s, 0, e * s);
+  // The leftover long tiles (in parts or not) beside rounds of short tiles on the other pairs, or
+  // split over all pairs before them. A step of 301 rows, 1032 x 2056 (10 long, 135 short tiles):
+  // 59.6 us in parts beside, 63.5 over all pairs; 64 rows of 2560 x 1024: 49.8 and 55.5.
+  int dummy = 1;
+  double best = rounds_cost(e, 0, &dummy) + rounds_cost(count[1], 1, &dummy);
+  int best_s = 0;
+  long long best_beside = 0;
+  const double small = tile_cycles(len[1], 1, bn, 1);
+  for (int s = 1; e * s < R && s <= std::min(len[0], 16); ++s) {
+    const int others = R - e * s;
+    const double t = tile_cycles(len[0], s, bn, used[0]);
+    const long long want = std::max(1LL, (long long)(t / small + 0.5)) * others;
+    const long long beside = std::min(want, count[1]);
+    const double c = std::max(t, (beside + others - 1) / others * small) +
+                     rounds_cost(count[1] - beside, 1, &dummy);
+    if (c < best) {
+      best = c;
+      best_s = s;
+      best_beside = beside;
     }
   }
+  if (!best_s) {
+    rounds(count[0], 0);
+    rounds(count[1], 1);
+    return g;
+  }
+  rounds(count[0] - e, 0);
+  g.cost += best;
+  add(e, best_s, 0, e * best_s);
+  add(best_beside, 1, e * best_s, R - e * best_s);
+  const double so_far = g.cost;
+  rounds(count[1] - best_beside, 1);
+  g.cost = so_far;
   return g;
 }
 
