@@ -162,6 +162,32 @@ def test_a_long_step_repeats_bit_for_bit(B):
         assert_norm_close(first[n], ref[n][0], BF, n)
 
 
+def test_the_most_rows(B):
+    """2^20 rows: h, dg and du have more than 2^31 values, the kept g and u more than 2^34 bytes. dy
+    is zero but in three stretches (the first rows, some in the middle, the last), so that the
+    weights' gradients are sums over those alone: the other rows add exact zeros."""
+    T, d, f = 1 << 20, 16, 2056
+    block, W = make(B, d, f)
+    desc = block.descriptor(T)
+    at = torch.cat([torch.arange(s, s + 150) for s in (0, T // 2 - 70, T - 150)]).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(BF)
+    dy = torch.zeros(T, d, dtype=BF, device="cuda")
+    dy[at] = rows(len(at), d, BF, seed=4)
+    ws, pre = B.alloc_ffn_workspace(desc, backward=True), B.ffn_pre(desc)
+    y = B.ffn_forward(desc, x, ws, pre=pre)
+    dx, *dw = B.ffn_backward(desc, x, dy, pre, ws)
+    assert B.ffn_device_status(desc, ws) == (0, 0)
+    del pre, ws
+    ref = ffn_ref(x[at], *W, "silu", BF, dy=dy[at])
+    for n, got in zip(("y", "dx", "dw_gate", "dw_up", "dw_down"), (y[at], dx[at], *dw)):
+        assert_close(got, *ref[n], BF, n)
+        assert_norm_close(got, ref[n][0], BF, n)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert (dx[rest] == 0).all()
+
+
 def test_only_what_is_asked_for_is_computed(B):
     T, d, f = 200, 136, 264
     block, W = make(B, d, f)

@@ -79,6 +79,34 @@ def test_many_outputs_with_k_in_parts(B):
         check(y[:, rows], x, dequantise(codes[rows], scales[rows], 128), None, 128, at)
 
 
+def test_a_matrix_beyond_32_bits(B):
+    """Codes of more than 2^32 bytes."""
+    N, K = 600_011, 16384
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=gen, device="cuda",
+                          dtype=torch.int32)
+    scales = (torch.rand(N, K // 64, generator=gen, device="cuda") * 2.0 ** -8 + 2.0 ** -9).to(BF)
+    m = B.QuantMatrix(codes, scales, K, 64)
+    for T in (1, 8):
+        x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(BF)
+        desc = m.descriptor(T, y_dtype=F32)
+        y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+        for at in (0, 2 ** 32 // (K // 2) - 100, N - 500):
+            part = slice(at, at + 500)
+            W = dequantise(codes[part].cpu(), scales[part].cpu(), 64)
+            check(y[:, part], x, W, None, 64, f"{T} rows, from {at}")
+
+
+def test_rows_far_apart(B):
+    """Rows of x and y 2^30 elements apart, the last beyond 2^32 bytes."""
+    T, N, K, ld = 4, 1000, 640, 1 << 30
+    desc, x, W, b = make(B, T, N, K, 128, ldx=ld, ldy=ld)
+    xb = torch.empty((T - 1) * ld + K, dtype=BF, device="cuda").as_strided((T, K), (ld, 1))
+    yb = torch.empty((T - 1) * ld + N, dtype=BF, device="cuda").as_strided((T, N), (ld, 1))
+    xb.copy_(x)
+    check(B.matvec(desc, xb, B.alloc_matvec_workspace(desc), out=yb), x, W, b, 128)
+
+
 # ---- calls large enough for the products on shifted codes (few rows, groups of 128): the sums
 # are sum((q + 8) x) - 8 sum(x), so their terms' magnitudes are those of |q| + 8
 
