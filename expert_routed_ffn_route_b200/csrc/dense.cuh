@@ -114,7 +114,9 @@ struct GemvArgs {
 
 // Bytes of partial sums and number of counters a call needs (0 when K is not split).
 void gemv_scratch(const GemvArgs& a, size_t* partial_bytes, size_t* n_counters);
-cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool pdl);
+// early: the kernel before in the stream is one of these that writes no weights (their copies then
+// start before it ends).
+cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool early);
 
 // ------------------------------------------------------------------ tensor-core kernels
 

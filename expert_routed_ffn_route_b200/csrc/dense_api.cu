@@ -120,7 +120,7 @@ moe_status ffn_validate(const moe_ffn* F) {
 }
 
 // Up to 32 rows the weights are streamed through the GEMV kernels (32 rows bf16: 2560 x 10240 46 us
-// against 58 on the tensor cores, 512 x 1024 13.0 against 13.5); a call that keeps g and u for a
+// against 59 on the tensor cores, 512 x 1024 12.5 in both); a call that keeps g and u for a
 // backward pass takes the tensor-core kernels at any T (they write them).
 inline bool streams(const moe_ffn* F, const void* pre) {
   return !is_16bit(F) || (F->T <= kGemvMaxRows && !pre);

@@ -337,8 +337,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Launched before the kernel ahead has ended, whatever it is: nothing that another kernel may
+  // write or read is touched before this wait. The next kernel may then set itself up on the SMs
+  // that are free.
   pdl_wait();
-  pdl_trigger();  // the next kernel may set itself up on the SMs that are free
+  pdl_trigger();
   auto fail = [&](int site) {
     set_timeout(a.status, site);
     *abort_flag = 1;
@@ -747,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // ------------------------------------------------------------------ host side
 
 template <int BN, int EPI, bool F16, int ACT>
-cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pdl) {
+cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st) {
   using C = GemmCfg<BN, EPI>;
   auto kern = ffn_gemm_kernel<BN, EPI, F16, ACT>;
   static std::atomic<bool> done[kMaxDevices];
@@ -763,20 +766,19 @@ cudaError_t launch_kernel(const GemmArgs& a, int pairs, cudaStream_t st, bool pd
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int BN, int EPI>
-cudaError_t launch_types(const GemmArgs& a, bool f16, int act, int pairs, cudaStream_t st,
-                         bool pdl) {
+cudaError_t launch_types(const GemmArgs& a, bool f16, int act, int pairs, cudaStream_t st) {
   constexpr int S = MOE_ACT_SILU, G = MOE_ACT_GELU;
   if (EPI == EPI_STORE || act == S)
-    return f16 ? launch_kernel<BN, EPI, true, S>(a, pairs, st, pdl)
-               : launch_kernel<BN, EPI, false, S>(a, pairs, st, pdl);
+    return f16 ? launch_kernel<BN, EPI, true, S>(a, pairs, st)
+               : launch_kernel<BN, EPI, false, S>(a, pairs, st);
   if constexpr (EPI != EPI_STORE)
-    return f16 ? launch_kernel<BN, EPI, true, G>(a, pairs, st, pdl)
-               : launch_kernel<BN, EPI, false, G>(a, pairs, st, pdl);
+    return f16 ? launch_kernel<BN, EPI, true, G>(a, pairs, st)
+               : launch_kernel<BN, EPI, false, G>(a, pairs, st);
   return cudaErrorInvalidValue;
 }
 
@@ -965,7 +967,7 @@ GemmPlan plan_products(const Product* pr, int n, bool gated, int R) {
 size_t plan_bytes(const GemmPlan& g) { return (size_t)g.units * 2 * kBM * g.bn * sizeof(float); }
 
 template <int EPI>
-cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_t st, bool pdl) {
+cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_t st) {
   const int sms = device_sms();
   if (sms < 2) return cudaErrorInvalidDevice;
   const GemmPlan g = plan_products(pr, n, EPI == EPI_GATED, std::min(kMaxPairs, sms / 2));
@@ -1025,9 +1027,9 @@ cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_
   int pairs = 0;
   for (int i = 0; i < g.n_phases; ++i)
     pairs = std::max(pairs, g.ph[i].lo + std::min(g.ph[i].n, g.ph[i].count * g.ph[i].splits));
-  if (bn == 256) return launch_types<256, EPI>(a, f.f16, f.act, pairs, st, pdl);
-  if (bn == 128) return launch_types<128, EPI>(a, f.f16, f.act, pairs, st, pdl);
-  if constexpr (EPI != EPI_GRAD) return launch_types<64, EPI>(a, f.f16, f.act, pairs, st, pdl);
+  if (bn == 256) return launch_types<256, EPI>(a, f.f16, f.act, pairs, st);
+  if (bn == 128) return launch_types<128, EPI>(a, f.f16, f.act, pairs, st);
+  if constexpr (EPI != EPI_GRAD) return launch_types<64, EPI>(a, f.f16, f.act, pairs, st);
   return cudaErrorInvalidValue;
 }
 
@@ -1068,12 +1070,12 @@ size_t ffn_partial_bytes(bool backward) {
 
 cudaError_t launch_ffn_gate_up(const FfnArgs& f, cudaStream_t st) {
   const Product p = gate_up_product(f);
-  return run_products<EPI_GATED>(&p, 1, f, st, false);
+  return run_products<EPI_GATED>(&p, 1, f, st);
 }
 
 cudaError_t launch_ffn_down(const FfnArgs& f, cudaStream_t st) {
   const Product p = down_product(f);
-  return run_products<EPI_STORE>(&p, 1, f, st, true);
+  return run_products<EPI_STORE>(&p, 1, f, st);
 }
 
 cudaError_t launch_ffn_gate_grad(const FfnArgs& f, cudaStream_t st) {
@@ -1083,7 +1085,7 @@ cudaError_t launch_ffn_gate_grad(const FfnArgs& f, cudaStream_t st) {
   p.K[0] = f.d;
   p.M = f.T;
   p.N = f.f;
-  return run_products<EPI_GRAD>(&p, 1, f, st, false);
+  return run_products<EPI_GRAD>(&p, 1, f, st);
 }
 
 cudaError_t launch_ffn_grads(const FfnArgs& f, cudaStream_t st) {
@@ -1113,7 +1115,7 @@ cudaError_t launch_ffn_grads(const FfnArgs& f, cudaStream_t st) {
     q.N = cols;
     q.out = out[i];
   }
-  return run_products<EPI_STORE>(p, n, f, st, true);
+  return run_products<EPI_STORE>(p, n, f, st);
 }
 
 }  // namespace moe

@@ -74,7 +74,7 @@ struct GemvPlan {
   int sums;          // bytes of a unit's group sums
   int wpr;           // log2 of the warps that stage one row
   int depth;         // ring slots a warp
-  int pdl;           // launched to overlap the kernel before it
+  int early;         // the kernel before writes no weights
   int smem;
 };
 
@@ -122,7 +122,7 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   p.tiles_r = p.tiles % p.groups;
   p.wpr = 0;
   while ((kWarps >> (p.wpr + 1)) >= a.T) ++p.wpr;
-  p.pdl = 0;
+  p.early = 0;
   p.smem = p.depth * kRingSlot + xbytes + 2048;
   return p;
 }
@@ -364,15 +364,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       xs[(cr * p.cols + (row ^ (cr & 1))) * 4 + (ft ^ (fi & 2))] = w;
     }
   };
-  // The weights do not depend on the kernel before: with programmatic launch their copies start
-  // first, else the (shorter) rows' do.
-  if (p.pdl) start_ring();
+  // Every launch is programmatic: the CTA sets itself up while the kernel ahead ends, and touches
+  // nothing that this may write or read before pdl_wait (1 row of 1024 x 2560 3.5 us a call in a
+  // row of calls, 4.2 without; 32 rows of 10240 x 2560 14.4 and 15.5). A block's down kernel follows
+  // its gate/up kernel, which has waited for all before it when this one starts and writes no
+  // weights, so there the copies of the weights come first of all; elsewhere the (shorter) rows'.
   if (FMT == 4 && n_my > 0) scale_tile();
-  load_scales();
+  if (p.early) {
+    start_ring();
+    load_scales();
+  }
   pdl_wait();
   pdl_trigger();
+  if (!p.early) load_scales();
   fetch_x();
-  if (!p.pdl) start_ring();
+  if (!p.early) start_ring();
   put_x(MASKED);
   while (xrow < a.T) {
     fetch_x();
@@ -735,7 +741,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 template <int FMT, int GROUP, bool F16, int TC, bool GATED, bool MASKED = false>
-cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
+cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st) {
   auto kern = gemv_rows_kernel<FMT, GROUP, F16, TC, GATED, MASKED>;
   static std::atomic<bool> done[kMaxDevices];
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), done);
@@ -756,35 +762,35 @@ cudaError_t launch_one(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bo
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, a, p);
 }
 
 template <int FMT, int GROUP, bool F16, bool GATED>
-cudaError_t launch_tc(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
+cudaError_t launch_tc(const GemvArgs& a, const GemvPlan& p, cudaStream_t st) {
   switch (p.tc) {
     case 1:
       if constexpr (FMT == 4 && GROUP == 128)
-        if (p.masked) return launch_one<FMT, GROUP, F16, 1, GATED, true>(a, p, st, pdl);
-      return launch_one<FMT, GROUP, F16, 1, GATED>(a, p, st, pdl);
-    case 2: return launch_one<FMT, GROUP, F16, 2, GATED>(a, p, st, pdl);
-    case 3: return launch_one<FMT, GROUP, F16, 3, GATED>(a, p, st, pdl);
-    default: return launch_one<FMT, GROUP, F16, 4, GATED>(a, p, st, pdl);
+        if (p.masked) return launch_one<FMT, GROUP, F16, 1, GATED, true>(a, p, st);
+      return launch_one<FMT, GROUP, F16, 1, GATED>(a, p, st);
+    case 2: return launch_one<FMT, GROUP, F16, 2, GATED>(a, p, st);
+    case 3: return launch_one<FMT, GROUP, F16, 3, GATED>(a, p, st);
+    default: return launch_one<FMT, GROUP, F16, 4, GATED>(a, p, st);
   }
 }
 
 template <bool F16>
-cudaError_t launch_fmt(const GemvArgs& a, const GemvPlan& p, cudaStream_t st, bool pdl) {
+cudaError_t launch_fmt(const GemvArgs& a, const GemvPlan& p, cudaStream_t st) {
   if (a.fmt == 16)
-    return a.gated ? launch_tc<16, 128, F16, true>(a, p, st, pdl)
-                   : launch_tc<16, 128, F16, false>(a, p, st, pdl);
+    return a.gated ? launch_tc<16, 128, F16, true>(a, p, st)
+                   : launch_tc<16, 128, F16, false>(a, p, st);
   if (a.gated) {
     if constexpr (F16) return cudaErrorInvalidValue;  // int4 blocks take bf16 rows
-    else return launch_tc<4, 128, F16, true>(a, p, st, pdl);
+    else return launch_tc<4, 128, F16, true>(a, p, st);
   }
-  if (a.group == 128) return launch_tc<4, 128, F16, false>(a, p, st, pdl);
-  if (a.group == 64) return launch_tc<4, 64, F16, false>(a, p, st, pdl);
-  return launch_tc<4, 32, F16, false>(a, p, st, pdl);
+  if (a.group == 128) return launch_tc<4, 128, F16, false>(a, p, st);
+  if (a.group == 64) return launch_tc<4, 64, F16, false>(a, p, st);
+  return launch_tc<4, 32, F16, false>(a, p, st);
 }
 
 }  // namespace
@@ -818,13 +824,13 @@ void gemv_scratch(const GemvArgs& a, size_t* partial_bytes, size_t* n_counters) 
   *n_counters = p.parts > 1 ? p.tiles : 0;
 }
 
-cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool pdl) {
+cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool early) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   GemvPlan p = make_gemv_plan(a, sms);
-  p.pdl = pdl;
+  p.early = early;
   if (p.smem > kSmemMax || p.parts > sms) return cudaErrorInvalidValue;
-  return a.f16 ? launch_fmt<true>(a, p, st, pdl) : launch_fmt<false>(a, p, st, pdl);
+  return a.f16 ? launch_fmt<true>(a, p, st) : launch_fmt<false>(a, p, st);
 }
 
 }  // namespace moe

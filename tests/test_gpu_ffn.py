@@ -376,6 +376,92 @@ def test_captured_step_replayed_beside_another(B):
         assert B.ffn_device_status(c["desc"], c["ws"]) == (0, 0)
 
 
+def test_a_call_sees_what_the_kernels_before_it_wrote(B):
+    """Launches overlap the end of the kernel before them. Here that kernel writes the call's rows or
+    its weights: another call (which lets its successor start early), a copy, a fill; on one stream
+    and on two joined by events; eager, and captured and replayed. Each result has the bits that
+    the same calls give when each waits for the one before."""
+    d, f = 256, 264
+    gen = torch.Generator().manual_seed(21)
+    codes, scales = quantise(gen, d, d, 128)
+    proj = B.QuantMatrix(codes.cuda(), scales.cuda(), d)
+    up, down = rows(f, d, BF, 11, d ** -0.5), rows(d, f, BF, 12, f ** -0.5)
+    w = dict(gate=torch.empty(f, d, dtype=BF, device="cuda"),
+             up=torch.empty(f, d, dtype=BF, device="cuda"),
+             down=torch.empty(d, f, dtype=BF, device="cuda"))
+    target = B.DeviceFfn(dict(fmt="bf16", w_gate=w["gate"], w_up=w["up"], w_down=w["down"]), d, f)
+    maker_g, _ = make(B, d, 520, seed=31)           # its rows become gate weights [f, d]
+    maker_d, _ = make(B, f, 520, seed=32)           # ... down weights [d, f]
+    mg, md = maker_g.descriptor(f), maker_d.descriptor(d)
+    seeds_g = [rows(f, d, BF, 40 + i) for i in range(2)]
+    seeds_d = [rows(d, f, BF, 50 + i) for i in range(2)]
+    side = torch.cuda.Stream()
+    descs = {T: (target.descriptor(T), proj.descriptor(T)) for T in (1, 4, 20)}
+    big = target.descriptor(300)
+    xs = {T: rows(T, d, BF, T) for T in (1, 4, 20, 300)}
+    dy = rows(300, d, BF, 77)
+    ws = B.alloc_ffn_workspace(big, backward=True)
+    ws = torch.zeros(max(ws.numel(), *(B.ffn_workspace_size(D) for D in (mg, md)),
+                         *(B.ffn_workspace_size(D[0]) for D in descs.values())),
+                     dtype=torch.uint8, device="cuda")
+    side_ws = torch.zeros_like(ws)
+
+    def sequence(wait):
+        out = []
+
+        def call(fn, *a, **k):
+            r = fn(*a, **k)
+            wait()
+            return r
+        here = torch.cuda.current_stream()
+        for i in (0, 1):
+            call(w["up"].copy_, up)
+            for T, (D, P) in descs.items():
+                # gate weights, then down weights, from the call just before; down ones first
+                call(B.ffn_forward, md, seeds_d[i], ws, out=w["down"])
+                call(B.ffn_forward, mg, seeds_g[i], ws, out=w["gate"])
+                y = call(B.ffn_forward, D, xs[T], ws)
+                call(w["gate"].zero_)
+                call(w["gate"].copy_, up)
+                out.append(call(B.ffn_forward, D, y, ws))
+                call(B.ffn_forward, md, seeds_d[1 - i], ws, out=w["down"])
+                out.append(call(B.ffn_forward, D, out[-1], ws))
+                z = call(B.matvec, P, out[-1], ws)
+                out.append(call(B.matvec, P, z, ws))
+                side.wait_stream(here)              # another stream's call in between
+                with torch.cuda.stream(side):
+                    z2 = call(B.matvec, P, out[-1], side_ws)
+                here.wait_stream(side)
+                out.append(call(B.ffn_forward, D, z2, ws))
+                side.wait_stream(here)
+            call(w["down"].copy_, down)
+            pre = B.ffn_pre(big)
+            y = call(B.ffn_forward, big, xs[300], ws, pre=pre)
+            call(y.mul_, 0.5)
+            out += [y, *call(B.ffn_backward, big, xs[300], dy, pre, ws)]
+            call(pre.zero_)
+            call(B.ffn_forward, mg, seeds_g[i], ws, out=w["gate"])
+            y = call(B.ffn_forward, big, xs[300], ws, pre=pre)
+            out += [y, *call(B.ffn_backward, big, xs[300], y, pre, ws)]
+        return out
+    want = [t.clone() for t in sequence(torch.cuda.synchronize)]
+    assert all(torch.isfinite(t).all() for t in want)
+    for _ in range(20):
+        got = sequence(lambda: None)
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = sequence(lambda: None)
+    for _ in range(20):
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
+
+
 def test_refusals(B):
     block, _ = make(B, 128, 128)
     int4, _ = make(B, 128, 128, fmt="int4")
