@@ -829,8 +829,13 @@ bool block_map(CUtensorMap* m, const void* base, int rows, int cols, int ch, int
 
 // The schedule of a launch. Tile width and K splits by estimated cycles, from measured launches: an
 // SM takes in about 46 bytes a cycle (a step of 64 K values brings it (128 + BN / 2) * 128, more
-// than the MMA's 2 BN cycles allow for at every width), a tile takes 1500 more to start and
-// drain, and a split one 5000 for the fence and the count, 8 BN to write and 8 BN a part to read.
+// than the MMA's 2 BN cycles allow for at every width), and 16 of those that come from DRAM (an
+// operand is counted once for all tiles that share it; forward launches alone: counted for the
+// gradients too, those of 64 rows of 2560 x 10240 take 94 us instead of 91). A tile takes 1500 more
+// to start and drain, a split one 6000 + 20 BN for the fences and the count, 8 BN to write and
+// 5.5 BN a part to read. With and without the terms 20 BN and DRAM: forward, 64 rows of 2560 x 10240
+// 51.7 / 58.3 us, 301 rows of 4096 x 2048 30.7 / 35.2; gradients, 301 rows of 4096 x 2048 50.4 / 57.0,
+// but 64 rows of 4096 x 2048 44.8 / 42.1 and 200 of 2560 x 10240 100 / 96.
 struct GemmPlan {
   Phase ph[kMaxPhases];
   int n_phases, bn, units, slots, pairs;
@@ -838,20 +843,23 @@ struct GemmPlan {
   double cost;
 };
 
-double step_cycles(int bn) { return std::max(2.0 * bn, (128 + bn / 2) * 128 / 46.0); }
+// Cycles of a step that brings a CTA `cold` bytes from DRAM.
+double step_cycles(int bn, double cold) {
+  return std::max(std::max(2.0 * bn, (128 + bn / 2) * 128 / 46.0), cold / 16);
+}
 
 // Cycles of a tile of `steps` K steps in s parts; `used`: the share of the tile's area that holds
 // results (the rest is not exchanged).
-double tile_cycles(int steps, int s, int bn, double used) {
-  return (steps + s - 1) / s * step_cycles(bn) + 1500 +
-         (s > 1 ? 6000 + (8 * used + 5.5 * s) * bn : 0);
+double tile_cycles(int steps, int s, int bn, double used, double cold) {
+  return (steps + s - 1) / s * step_cycles(bn, cold) + 1500 +
+         (s > 1 ? 6000 + (20 + 8 * used + 5.5 * s) * bn : 0);
 }
 
 // Cycles of `r` tiles on R idle pairs, split the best way.
-double split_cost(int r, int steps, int R, int bn, double used, int* splits) {
+double split_cost(int r, int steps, int R, int bn, double used, double cold, int* splits) {
   double best = -1;
   for (int s = 1; s <= std::min(std::min(R / r, steps), 16); ++s) {
-    const double c = tile_cycles(steps, s, bn, used);
+    const double c = tile_cycles(steps, s, bn, used, cold);
     if (best < 0 || c < best) {
       best = c;
       *splits = s;
@@ -876,6 +884,10 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
   for (int i = 1; i < n; ++i)  // longest first, equal ones in order
     for (int j = i; j > 0 && steps[g.order[j]] > steps[g.order[j - 1]]; --j)
       std::swap(g.order[j], g.order[j - 1]);
+  double cold = 0;
+  if (!pr[0].b[0].mn)  // a forward launch: one product
+    cold = 128.0 * 128 / ((pr[0].N + cols - 1) / cols) +
+           bn / 2 * 128.0 / ((pr[0].M + kPairM - 1) / kPairM);
   // at most two lengths: the input gradient's and the weight gradients'
   long long count[2] = {0, 0};
   double area[2] = {0, 0};
@@ -909,8 +921,8 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
   // cnt tiles of length c over all pairs: whole rounds, then the rest split
   const auto rounds_cost = [&](long long cnt, int c, int* s) {
     const int rest = (int)(cnt % R);
-    return cnt / R * tile_cycles(len[c], 1, bn, 1) +
-           (rest ? split_cost(rest, len[c], R, bn, used[c], s) : 0);
+    return cnt / R * tile_cycles(len[c], 1, bn, 1, cold) +
+           (rest ? split_cost(rest, len[c], R, bn, used[c], cold, s) : 0);
   };
   const auto rounds = [&](long long cnt, int c) {
     int s = 1;
@@ -932,10 +944,10 @@ GemmPlan plan_width(const Product* pr, int n, bool gated, int R, int bn) {
   double best = rounds_cost(e, 0, &dummy) + rounds_cost(count[1], 1, &dummy);
   int best_s = 0;
   long long best_beside = 0;
-  const double small = tile_cycles(len[1], 1, bn, 1);
+  const double small = tile_cycles(len[1], 1, bn, 1, cold);
   for (int s = 1; e * s < R && s <= std::min(len[0], 16); ++s) {
     const int others = R - e * s;
-    const double t = tile_cycles(len[0], s, bn, used[0]);
+    const double t = tile_cycles(len[0], s, bn, used[0], cold);
     const long long want = std::max(1LL, (long long)(t / small + 0.5)) * others;
     const long long beside = std::min(want, count[1]);
     const double c = std::max(t, (beside + others - 1) / others * small) +
