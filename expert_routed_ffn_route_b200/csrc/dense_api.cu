@@ -119,9 +119,10 @@ moe_status ffn_validate(const moe_ffn* F) {
   return MOE_OK;
 }
 
-// Up to 32 rows the weights are streamed through the GEMV kernels (32 rows bf16: 2560 x 10240 46 us
-// against 59 on the tensor cores, 512 x 1024 12.5 in both); a call that keeps g and u for a
-// backward pass takes the tensor-core kernels at any T (they write them).
+// Up to 32 rows the weights are streamed through the GEMV kernels (32 rows bf16, streamed / on the
+// tensor cores: 2560 x 1024 16.0 / 18.5 us, 2560 x 10240 46 / 49, 512 x 1024 12.6 / 12.1; one shape
+// measured is better off there from 16 rows: 4096 x 4096 37.5 / 34.3, 4 rows 30.9 / 43.6); a call
+// that keeps g and u for a backward pass takes the tensor-core kernels at any T (they write them).
 inline bool streams(const moe_ffn* F, const void* pre) {
   return !is_16bit(F) || (F->T <= kGemvMaxRows && !pre);
 }

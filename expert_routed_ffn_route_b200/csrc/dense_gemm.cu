@@ -43,8 +43,8 @@
 // the status word and its site, and every role stops.
 //
 // Measured on one B200 (kernel time in graphs / in a steady loop under the power cap): forward of
-// 4096 rows, 2560 x 10240, 422 / 490 us (1527 / 1314 TFLOP/s; 1631 and 1375 are the measured
-// library peaks), training step 1.39 / 1.62 ms (1387 / 1193).
+// 4096 rows, 2560 x 10240, 422 / 490..500 us (1527 / 1300 TFLOP/s; 1631 and 1375 are the measured
+// library peaks), training step 1.39 / 1.62..1.68 ms (1387 / 1170).
 #include <cstring>
 
 #include "dense.cuh"
