@@ -516,17 +516,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[c][j] = head[c][j] = 0.f;
   const uint8_t* xp = xlane + slot0 * (2 * XI) * xstep;
-  // 2^133 / 2^100 (bf16) or 2^24 (fp16): the masked form's unit
-  const float unit = !(MASKED && masked) ? 1.f : F16 ? 16777216.f : 8589934592.f;
+  // 2^133 / 2^100 (bf16) or 2^24 (fp16): the masked form's unit. It goes into the group's sum, which
+  // is in range with it; a scale of 2^95 (2^104) or more times it would be infinite.
+  constexpr float unit = F16 ? 16777216.f : 8589934592.f;
   auto run = [&](auto fast) {
     constexpr bool FAST = decltype(fast)::value;
     for (int it = 0; it < n_my; ++it) {
       float sc[NSC];
 #pragma unroll
-      for (int j = 0; j < NSC; ++j) {
-        sc[j] = __uint_as_float(sn[j] << 16);
-        if constexpr (FAST) sc[j] *= unit;
-      }
+      for (int j = 0; j < NSC; ++j) sc[j] = __uint_as_float(sn[j] << 16);
       load_scales();
       const uint8_t* sp = ring + stage * kSlotBytes;
       if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
@@ -622,9 +620,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               const float s1 = __shfl_sync(0xffffffffu, sc[i / kWords], 2 + u, 4);
 #pragma unroll
               for (int n = 0; n < TC; ++n) {
-                if constexpr (FAST)
+                if constexpr (FAST)  // unit and unit / 16 are powers of two: one rounding
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) c[n][j] = fmaf(0.0625f, ch[n][j], c[n][j]);
+                  for (int j = 0; j < 4; ++j)
+                    c[n][j] = fmaf(unit * 0.0625f, ch[n][j], unit * c[n][j]);
                 acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
                 acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
                 acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);

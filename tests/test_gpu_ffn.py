@@ -527,3 +527,25 @@ def test_layer_block_and_projection_in_one_captured_step(B):
     assert_close(out[1], ref, bound, BF, "block")
     ref, mag = matvec_ref(out[1].cpu(), dequantise(codes, scales, 64))
     assert_close(out[2], ref, mag * matvec_additions(256, 64) * 2.0 ** -23, F32, "projection")
+
+
+@pytest.mark.parametrize("T", [1, 8])
+def test_large_int4_block_with_large_scales(B, T):
+    """Gate and up scales of 2^95 and more with rows around 2^-89: gates of ordinary size (2^14), in a
+    block large enough for the products on shifted codes."""
+    d, f = 2560, 4096
+    gen = torch.Generator().manual_seed(13)
+    bank, W = dict(fmt="int4", group=128, n_exp=1), []
+    for m, N, K, by in (("gate", f, d, 2.0 ** 103), ("up", f, d, 2.0 ** 103), ("down", d, f, 1.0)):
+        codes, scales = quantise(gen, N, K, 128)
+        scales = (scales.double() * by).to(BF)
+        bank["w_" + m], bank["s_" + m] = codes.cuda(), scales.cuda()
+        W.append(dequantise(codes, scales, 128).cuda())
+    x = 1 + torch.rand(T, d, generator=gen)
+    x = (x * 2.0 ** -89 * (1 - 2 * torch.randint(0, 2, (T, d), generator=gen))).to(BF).cuda()
+    desc = B.DeviceFfn(bank, d, f).descriptor(T)
+    y = B.ffn_forward(desc, x, B.alloc_ffn_workspace(desc))
+    assert torch.isfinite(y).all()
+    ref, bound = ffn_ref(x, *W, "silu", BF)["y"]
+    assert_close(y, ref, bound, BF, "y")
+    assert_norm_close(y, ref, BF, "y")

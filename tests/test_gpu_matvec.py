@@ -325,3 +325,26 @@ def test_same_encoding_as_an_expert_bank(B):
                    torch.from_numpy(arrays["s_down"][2].view("int16")).view(BF), 128)
     assert W.shape == (cfg.d, cfg.f) and O is not None
     check(y, x, W, None, 128)
+
+
+@pytest.mark.parametrize("x_dtype,scale,value", [
+    (BF, 2.0 ** 94, 2.0 ** -40), (BF, 2.0 ** 95, 2.0 ** -60), (BF, 2.0 ** 127, 2.0 ** -85),
+    (BF, 2.0 ** -126, 2.0 ** 20), (BF, 2.0 ** -133, 2.0 ** 24),
+    (HF, 2.0 ** 103, 2.0 ** -8), (HF, 2.0 ** 104, 2.0 ** -12), (HF, 2.0 ** 127, 2.0 ** -14),
+    (HF, 2.0 ** -126, 2.0 ** 12)])
+@pytest.mark.parametrize("T", [1, 8])
+def test_large_matrix_scales_at_the_ends_of_their_type(B, big, T, x_dtype, scale, value):
+    """Scales up to bf16's largest binade and down to its subnormals, beside rows (inside the
+    shifted form's range) that bring the results back to fp32's: every result is finite and as
+    exact as with ordinary scales."""
+    m, _, scales = big
+    codes, (N, K) = m.codes.cpu(), BIG
+    s = (torch.frexp(scales.float())[0].double() * 2 * scale).to(BF)   # [1, 2) times scale
+    assert torch.isfinite(s).all()
+    gen = torch.Generator().manual_seed(12)
+    x = 1 + torch.rand(T, K, generator=gen)
+    x = (x * value * (1 - 2 * torch.randint(0, 2, (T, K), generator=gen))).to(x_dtype)
+    desc = B.QuantMatrix(m.codes, s.cuda(), K).descriptor(T, x_dtype=x_dtype, y_dtype=F32)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+    assert torch.isfinite(y).all()
+    check_shifted(y, x, dequantise(codes, s, 128), s)
