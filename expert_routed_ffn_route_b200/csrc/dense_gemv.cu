@@ -292,7 +292,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     --sleft;
     const int at = (begin + 2 * ss + (t4 & 1)) * NSC;
 #pragma unroll
-    for (int j = 0; j < NSC; ++j) sn[j] = __ldg(srow + min(at + j, n_scales - 1));
+    for (int j = 0; j < NSC; ++j) {
+      // behind the last group (K need not fill a unit) the sum is zero, and so is the scale: the last
+      // group's own may be infinite
+      if (GROUP == 128) sn[j] = __ldg(srow + min(at + j, n_scales - 1));
+      else sn[j] = at + j < n_scales ? __ldg(srow + at + j) : 0;
+    }
     if (++ss == n_slots) {
       ss = 0;
       ++st;

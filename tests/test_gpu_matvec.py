@@ -348,3 +348,20 @@ def test_large_matrix_scales_at_the_ends_of_their_type(B, big, T, x_dtype, scale
     y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
     assert torch.isfinite(y).all()
     check_shifted(y, x, dequantise(codes, s, 128), s)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("K,group", [(32, 32), (416, 32), (192, 64), (320, 64)])
+def test_an_infinite_scale_of_the_last_group(B, T, K, group):
+    """K that ends inside a unit of 128: what lies behind the last group takes no part, its scale's
+    infinity neither (it would meet a sum of zero)."""
+    N = 40
+    gen = torch.Generator().manual_seed(K)
+    q = torch.randint(1, 8, (N, K), generator=gen)
+    scales = torch.full((N, K // group), 0.5).to(BF)
+    scales[::2, -1] = float("inf")
+    x = (torch.rand(T, K, generator=gen) + 0.5).to(BF)
+    desc = B.QuantMatrix(pack(q).cuda(), scales.cuda(), K, group).descriptor(T, y_dtype=F32)
+    y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc)).cpu()
+    assert (y[:, ::2] == float("inf")).all()
+    check(y[:, 1::2], x, dequantise(pack(q)[1::2], scales[1::2], group), None, group)
