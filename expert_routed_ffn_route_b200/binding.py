@@ -368,7 +368,9 @@ def test_inject_hold(L: MoeLayer, ws, hold: bool, budget_cycles: int = 0, stream
 #
 # Unlike the layer's calls above, these check their tensors (type, shape, layout, device)
 # before handing over pointers, and raise ValueError. The work runs on the tensors' device,
-# on its current stream unless one is given.
+# on its current stream unless one is given. A given stream is the current one during the call:
+# its work comes after what that stream holds, results belong to it, and a caller who goes on on
+# another stream orders the two as with torch.cuda.stream.
 
 
 def _dtype_code(t) -> int:
@@ -400,20 +402,41 @@ def _check_ws(ws, index):
 _CURRENT = None  # (current device, its raw stream), bound at the first call
 
 
-def _call(index, stream, fn, *args):
-    """fn(*args, stream) with CUDA device `index` current; returns its status. The current stream
-    is asked for as a raw handle: building a torch stream object takes as long as a kernel
-    launch."""
+def _call(index, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current, on its current stream; returns its status.
+    The stream is asked for as a raw handle: building a torch stream object takes as long as a
+    kernel launch."""
     global _CURRENT
     if _CURRENT is None:
         import torch
         _CURRENT = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     current_device, raw_stream = _CURRENT
     if index == current_device():
-        return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
+        return fn(*args, raw_stream(index))
     import torch
     with torch.cuda.device(index):
-        return fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
+        return fn(*args, raw_stream(index))
+
+
+def _on(stream, fn, *args, **kwargs):
+    """fn(*args, **kwargs) with the given `stream` current, so that its results are allocated for
+    that stream (a block of another stream's pool may still be in use by what is queued there).
+    What the call reads and writes is marked as used by the stream: freed early, it is not handed
+    out again before the stream is done with it."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    for a in (*args, *kwargs.values()):
+        owner = getattr(a, "owner", None)  # a descriptor: its weights
+        held = (a,) if owner is None else (*vars(owner).values(), *getattr(owner, "bank", {}).values())
+        for t in held:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                if t.get_device() != stream.device_index:
+                    raise ValueError(f"the stream is on cuda:{stream.device_index}, a tensor of the "
+                                     f"call on {t.device}")
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
 
 
 def _alloc_zeroed(nbytes: int, device):
@@ -476,6 +499,8 @@ def alloc_matvec_workspace(M: MoeMatrix):
 
 def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     """y = x W^T (+ bias) for the T <= 32 rows of x: [T, K] -> [T, N] (include/moe_b200.h)."""
+    if stream is not None:
+        return _on(stream, matvec, M, x, ws, out)
     x_shape, y_shape, ldx, ldy, xt, yt, index, ref, fn = M.call
     _check_rows(x, "x", x_shape, xt, index, ldx)
     if out is None:
@@ -487,7 +512,7 @@ def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     else:
         _check_rows(out, "out", y_shape, yt, index, ldy)
     _check_ws(ws, index)
-    status = _call(index, stream, fn, ref, x.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+    status = _call(index, fn, ref, x.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
     if status:
         _check(status, "moe_matvec")
     return out
@@ -572,6 +597,8 @@ def _check_pre(pre, shape, index):
 def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     """y = Wd (act(Wg x) * (Wu x)) for the rows of x [T, d]; ``pre`` (ffn_pre) keeps what
     ffn_backward needs (include/moe_b200.h)."""
+    if stream is not None:
+        return _on(stream, ffn_forward, F, x, ws, out, pre)
     shape, pre_shape, dtype, index, ref, fn, _ = F.call
     _check_rows(x, "x", shape, dtype, index)
     if out is None:
@@ -581,7 +608,7 @@ def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     if pre is not None:
         _check_pre(pre, pre_shape, index)
     _check_ws(ws, index)
-    status = _call(index, stream, fn, ref, x.data_ptr(), out.data_ptr(), _ptr(pre), ws.data_ptr(),
+    status = _call(index, fn, ref, x.data_ptr(), out.data_ptr(), _ptr(pre), ws.data_ptr(),
                    ws.numel())
     if status:
         _check(status, "moe_ffn_forward")
@@ -592,6 +619,8 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
                  stream=None):
     """(dx, dw_gate, dw_up, dw_down) from dy [T, d], x and the ``pre`` of ffn_forward; what is
     not needed is None and not computed. ``ws``: alloc_ffn_workspace(F, backward=True)."""
+    if stream is not None:
+        return _on(stream, ffn_backward, F, x, dy, pre, ws, need_dx, need_dw)
     shape, pre_shape, dtype, index, ref, _, fn = F.call
     _check_rows(x, "x", shape, dtype, index)
     _check_rows(dy, "dy", shape, dtype, index)
@@ -601,14 +630,16 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
     dwg = dwu = dwd = None
     if need_dw:
         dwg, dwu, dwd = x.new_empty(F.f, F.d), x.new_empty(F.f, F.d), x.new_empty(F.d, F.f)
-    _check(_call(index, stream, fn, ref, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), _ptr(dx),
+    _check(_call(index, fn, ref, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), _ptr(dx),
                  _ptr(dwg), _ptr(dwu), _ptr(dwd), ws.data_ptr(), ws.numel()), "moe_ffn_backward")
     return dx, dwg, dwu, dwd
 
 
 def _device_status(fn, D, ws, stream):
+    if stream is not None:
+        return _on(stream, _device_status, fn, D, ws, None)
     code, site = ctypes.c_int32(0), ctypes.c_int32(0)
-    _check(_call(D.owner.device.index, stream, fn, ctypes.byref(D), ws.data_ptr(), ws.numel(),
+    _check(_call(D.owner.device.index, fn, ctypes.byref(D), ws.data_ptr(), ws.numel(),
                  ctypes.byref(code), ctypes.byref(site)), fn.__name__)
     return code.value, site.value
 

@@ -212,3 +212,56 @@ def test_ffn_struct_layout_matches_the_header(tmp_path):
     sizes = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
                                             check=True).stdout.split()]
     assert sizes == [ctypes.sizeof(binding.MoeFfn), binding.MoeFfn.bank.offset]
+
+
+class FakeStream:
+    cuda_stream, device_index = 77, -1
+
+
+def calls_on_a_fake_device(monkeypatch):
+    """The binding's calls with CPU tensors, a library that accepts everything and a fake CUDA
+    runtime. Returns (allocations, launches, torch): the raw stream that was current at each."""
+    import contextlib
+    torch = pytest.importorskip("torch")
+    current, allocations, launches = [0], [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s.cuda_stream
+        yield
+        current[0] = before
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(binding, "_CURRENT", (lambda: -1, lambda index: current[0]))
+    new_empty = torch.Tensor.new_empty
+
+    def noted(self, *args, **kwargs):
+        allocations.append(current[0])
+        return new_empty(self, *args, **kwargs)
+    monkeypatch.setattr(torch.Tensor, "new_empty", noted)
+
+    def accept(*args):
+        launches.append(args[-1])
+        return 0
+    return allocations, launches, accept, torch
+
+
+@pytest.mark.parametrize("stream", [None, FakeStream()])
+def test_results_are_allocated_for_the_stream_of_the_call(monkeypatch, stream):
+    """A result from the current stream's memory, written on another stream, could be a block that
+    queued work of the current stream still reads."""
+    from types import SimpleNamespace
+    allocations, launches, accept, torch = calls_on_a_fake_device(monkeypatch)
+    bf = torch.bfloat16
+    ws = torch.zeros(256, dtype=torch.uint8)
+    M = SimpleNamespace(call=((2, 8), (2, 4), 8, 4, bf, bf, -1, None, accept))
+    x = torch.zeros(2, 8, dtype=bf)
+    y = binding.matvec(M, x, ws, stream=stream)
+    assert y.shape == (2, 4)
+    F = SimpleNamespace(call=((2, 8), (2, 2, 16), bf, -1, None, accept, accept), d=8, f=16)
+    pre = torch.zeros(2, 2, 16)
+    y = binding.ffn_forward(F, x, ws, pre=pre, stream=stream)
+    grads = binding.ffn_backward(F, x, y, pre, ws, stream=stream)
+    assert [tuple(g.shape) for g in grads] == [(2, 8), (16, 8), (16, 8), (8, 16)]
+    want = 0 if stream is None else stream.cuda_stream
+    assert allocations == [want] * 6 and launches == [want] * 3

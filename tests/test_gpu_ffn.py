@@ -549,3 +549,42 @@ def test_large_int4_block_with_large_scales(B, T):
     ref, bound = ffn_ref(x, *W, "silu", BF)["y"]
     assert_close(y, ref, bound, BF, "y")
     assert_norm_close(y, ref, BF, "y")
+
+
+def test_a_step_on_a_given_stream_keeps_to_its_memory(B):
+    """As for the matrix: results of a step on another stream do not come from blocks that the
+    current stream still reads, and its temporaries may be dropped at once."""
+    T, d, f = 200, 1024, 2048
+    block, _ = make(B, d, f)
+    x, dy = rows(T, d, BF), rows(T, d, BF, seed=2)
+    desc = block.descriptor(T)
+
+    def step(stream):
+        ws, pre = B.alloc_ffn_workspace(desc, backward=True), B.ffn_pre(desc)
+        y = B.ffn_forward(desc, x, ws, pre=pre, stream=stream)
+        return (y, *B.ffn_backward(desc, x, dy, pre, ws, stream=stream))
+    want = [t.clone() for t in step(None)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        blocks = [torch.full(t.shape, 5.0, dtype=BF, device="cuda") for t in want]
+        ws, pre = B.alloc_ffn_workspace(desc, backward=True), B.ffn_pre(desc)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(10_000_000)
+        torch.cuda._sleep(20_000_000)
+        copies = [torch.empty_like(t).copy_(t) for t in blocks]
+        del blocks
+        y = B.ffn_forward(desc, x, ws, pre=pre, stream=side)
+        got = (y, *B.ffn_backward(desc, x, dy, pre, ws, stream=side))
+        n = ws.numel(), pre.shape
+        del ws, pre
+        junk = [torch.full((n[0],), 255, dtype=torch.uint8, device="cuda"),
+                torch.full(n[1], 9.0, device="cuda")]
+        torch.cuda.synchronize()
+        assert all((c == 5).all() for c in copies) and len(junk) == 2
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError):
+            B.ffn_forward(desc, x, B.alloc_ffn_workspace(desc), stream=torch.cuda.Stream(device=1))

@@ -365,3 +365,36 @@ def test_an_infinite_scale_of_the_last_group(B, T, K, group):
     y = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc)).cpu()
     assert (y[:, ::2] == float("inf")).all()
     check(y[:, 1::2], x, dequantise(pack(q)[1::2], scales[1::2], group), None, group)
+
+
+def test_calls_on_a_given_stream_keep_to_their_memory(B):
+    """Blocks that the current stream has freed but whose readers are still queued there are not
+    handed out as results on another stream, and what a call on another stream uses is not handed
+    out again, when freed at once, before that call has run."""
+    T, N, K = 32, 8192, 2560
+    desc, x, W, b = make(B, T, N, K, 128)
+    want = B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc))
+    here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    for _ in range(3):
+        side.wait_stream(here)
+        torch.cuda.synchronize()
+        # a reader of a freed block queued here, behind a pause
+        block = torch.full((T, N), 5.0, dtype=BF, device="cuda")
+        xd, ws = x.cuda(), B.alloc_matvec_workspace(desc)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        copy = torch.empty_like(block).copy_(block)
+        del block
+        y = B.matvec(desc, xd, ws, stream=side)
+        torch.cuda.synchronize()
+        assert (copy == 5).all() and torch.equal(y, want)
+        # the call's own tensors, freed while it waits behind a pause on its stream
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        y = B.matvec(desc, xd, ws, stream=side)
+        shape = xd.shape, ws.shape
+        del xd, ws
+        junk = [torch.full(shape[0], 9.0, dtype=BF, device="cuda") for _ in range(4)]
+        junk += [torch.full(shape[1], 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and B.matvec_device_status(desc, junk[-1].zero_()) == (0, 0)
