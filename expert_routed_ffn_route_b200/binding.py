@@ -6,6 +6,7 @@ shared library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -226,10 +227,23 @@ def alloc_workspace(L: MoeLayer, device="cuda"):
     return ws
 
 
+def _on_stream(stream):
+    """The context in which a call's results are allocated: with a given stream current, so that
+    their memory is that stream's (a block of another stream's pool may still be in use by what is
+    queued there). Tensors that the caller brings are the caller's to keep and to order."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def route(L: MoeLayer, x, ws, stream=None):
     import torch
-    idx = torch.empty((L.T, L.k), dtype=torch.int32, device=x.device)
-    w = torch.empty((L.T, L.k), dtype=torch.float32, device=x.device)
+    with _on_stream(stream):
+        idx = torch.empty((L.T, L.k), dtype=torch.int32, device=x.device)
+        w = torch.empty((L.T, L.k), dtype=torch.float32, device=x.device)
     _check(load_library().moe_route(ctypes.byref(L), x.data_ptr(), idx.data_ptr(), w.data_ptr(),
                                     ws.data_ptr(), ws.numel(), _stream(stream)), "moe_route")
     return idx, w
@@ -238,9 +252,10 @@ def route(L: MoeLayer, x, ws, stream=None):
 def permute(L: MoeLayer, topk_idx, ws, stream=None):
     import torch
     dev = topk_idx.device
-    offsets = torch.empty(L.E + 1, dtype=torch.int32, device=dev)
-    perm = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
-    inv = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
+    with _on_stream(stream):
+        offsets = torch.empty(L.E + 1, dtype=torch.int32, device=dev)
+        perm = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
+        inv = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
     _check(load_library().moe_permute(ctypes.byref(L), topk_idx.data_ptr(), offsets.data_ptr(),
                                       perm.data_ptr(), inv.data_ptr(), ws.data_ptr(), ws.numel(),
                                       _stream(stream)), "moe_permute")
@@ -250,8 +265,9 @@ def permute(L: MoeLayer, topk_idx, ws, stream=None):
 def grouped_ffn(L: MoeLayer, x, offsets, perm, ws, has_shared=True, stream=None):
     import torch
     dev = x.device
-    y_assign = torch.empty((L.T * L.k, L.d), dtype=torch.float32, device=dev)
-    y_shared = torch.empty((L.T, L.d), dtype=torch.float32, device=dev) if has_shared else None
+    with _on_stream(stream):
+        y_assign = torch.empty((L.T * L.k, L.d), dtype=torch.float32, device=dev)
+        y_shared = torch.empty((L.T, L.d), dtype=torch.float32, device=dev) if has_shared else None
     _check(load_library().moe_grouped_ffn(ctypes.byref(L), x.data_ptr(), offsets.data_ptr(),
                                           perm.data_ptr(), y_assign.data_ptr(), _ptr(y_shared),
                                           ws.data_ptr(), ws.numel(), _stream(stream)),
@@ -262,7 +278,8 @@ def grouped_ffn(L: MoeLayer, x, offsets, perm, ws, has_shared=True, stream=None)
 def combine(L: MoeLayer, y_assign, y_shared, inv, topk_w, out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=y_assign.device)
+        with _on_stream(stream):
+            out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=y_assign.device)
     _check(load_library().moe_combine(ctypes.byref(L), y_assign.data_ptr(), _ptr(y_shared),
                                       inv.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
                                       _stream(stream)), "moe_combine")
@@ -274,7 +291,8 @@ def layer_forward(L: MoeLayer, x, ws, out=None, topk_idx=None, topk_w=None, offs
     """The fused layer call. Optional outputs are written when tensors are given."""
     import torch
     if out is None:
-        out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
+        with _on_stream(stream):
+            out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
     lib = load_library()
     if marks is None:
         st = lib.moe_layer_forward(ctypes.byref(L), x.data_ptr(), out.data_ptr(), _ptr(topk_idx),
@@ -294,8 +312,9 @@ def nvfp4_pack_scales(src, n_mats: int, rows: int, K: int, stream=None):
     """Block scales of an NVFP4 bank, uint8 [n_mats][rows][K/16] on the device, rearranged
     into the layout the FP4 tensor-core kernels read (a new tensor of the same size)."""
     import torch
-    src = src.contiguous()
-    dst = torch.empty_like(src)
+    with _on_stream(stream):
+        src = src.contiguous()
+        dst = torch.empty_like(src)
     _check(load_library().moe_nvfp4_pack_scales(src.data_ptr(), dst.data_ptr(), n_mats, rows, K,
                                                 _stream(stream)), "moe_nvfp4_pack_scales")
     return dst
@@ -305,11 +324,12 @@ def nvfp4_quantize_rows(v, stream=None):
     """fp32 rows [R, K] on the device -> (E2M1 codes uint8 [R, K/2], E4M3 block-scale codes
     uint8 [R, K/16], fp32 row scales [R]) by the layer's activation quantiser."""
     import torch
-    v = v.contiguous()
     R, K = v.shape
-    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=v.device)
-    scales = torch.empty((R, K // 16), dtype=torch.uint8, device=v.device)
-    g = torch.empty(R, dtype=torch.float32, device=v.device)
+    with _on_stream(stream):
+        v = v.contiguous()
+        codes = torch.empty((R, K // 2), dtype=torch.uint8, device=v.device)
+        scales = torch.empty((R, K // 16), dtype=torch.uint8, device=v.device)
+        g = torch.empty(R, dtype=torch.float32, device=v.device)
     _check(load_library().moe_nvfp4_quantize_rows(v.data_ptr(), R, K, codes.data_ptr(),
                                                   scales.data_ptr(), g.data_ptr(),
                                                   _stream(stream)), "moe_nvfp4_quantize_rows")
@@ -342,7 +362,8 @@ def layer_forward_static(L: MoeLayer, x, out=None, stream=None):
     that cannot allocate device memory. Limits and sharing rules: include/moe_b200.h."""
     import torch
     if out is None:
-        out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
+        with _on_stream(stream):
+            out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
     _check(load_library().moe_layer_forward_static(ctypes.byref(L), x.data_ptr(),
                                                    out.data_ptr(), _stream(stream)),
            "moe_layer_forward_static")

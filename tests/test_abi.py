@@ -188,3 +188,45 @@ def test_header_is_plain_c(tmp_path):
                                             check=True).stdout.split()]
     assert sizes == [ctypes.sizeof(binding.MoeBank), ctypes.sizeof(binding.MoeLayer),
                      binding.MoeLayer.routed.offset, binding.MoeBank.g_gate.offset]
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_results_are_allocated_for_the_stream_of_the_call(monkeypatch, given):
+    """With a given stream, what a call returns is that stream's memory: a block of the current
+    stream's pool could still be in use by what is queued there."""
+    import contextlib
+    from types import SimpleNamespace
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 77
+    current, at = [0], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s.cuda_stream
+        yield
+        current[0] = before
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: SimpleNamespace(cuda_stream=current[0]))
+    for name in ("empty", "empty_like"):
+        def noted(*args, fn=getattr(torch, name), **kwargs):
+            at.append(current[0])
+            return fn(*args, **kwargs)
+        monkeypatch.setattr(torch, name, noted)
+    lib = type("Lib", (), {"__getattr__": lambda self, name: lambda *args: 0})()
+    monkeypatch.setattr(binding, "load_library", lambda: lib)
+    L = binding.MoeLayer(3, 64, 64, 4, 2, 0, None, None, binding.bank_struct(None),
+                         binding.bank_struct(None))
+    s = Stream() if given else None
+    ws, x = torch.zeros(8, dtype=torch.uint8), torch.zeros(3, 64, dtype=torch.bfloat16)
+    idx, w = binding.route(L, x, ws, stream=s)
+    offsets, perm, inv = binding.permute(L, idx, ws, stream=s)
+    y, ys = binding.grouped_ffn(L, x, offsets, perm, ws, stream=s)
+    binding.combine(L, y, ys, inv, w, stream=s)
+    binding.layer_forward(L, x, ws, stream=s)
+    binding.layer_forward_static(L, x, stream=s)
+    binding.nvfp4_pack_scales(torch.zeros(2, 128, 4, dtype=torch.uint8), 2, 128, 64, stream=s)
+    binding.nvfp4_quantize_rows(torch.zeros(4, 64), stream=s)
+    assert at == [77 if given else 0] * 14 and current == [0]

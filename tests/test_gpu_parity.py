@@ -299,3 +299,23 @@ def test_fused_unsupported_reported(B):
     with pytest.raises(B.MoeError) as e:
         B.layer_forward(desc, to_dev_x(L.x), ws)
     assert e.value.status == -2
+
+
+def test_a_call_on_a_given_stream_leaves_freed_blocks_alone(B):
+    """A block that the current stream freed while its reader is still queued there is not handed
+    out as the result of a call on another stream."""
+    L = synth.make_layer("tiny")
+    dl = B.DeviceLayer(L)  # (the layer's descriptor does not keep the weights)
+    desc = dl.descriptor(L.cfg.T)
+    x, ws = to_dev_x(L.x), B.alloc_workspace(desc)
+    want = B.layer_forward(desc, x, ws)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        block = torch.full_like(want, 5.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        copy = torch.empty_like(block).copy_(block)
+        del block
+        out = B.layer_forward(desc, x, ws, stream=side)
+        torch.cuda.synchronize()
+        assert (copy == 5).all() and torch.equal(out, want)
