@@ -24,6 +24,19 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return a && b && an && bn && x < y + bn && y < x + an;
 }
 
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Whether one of the first n_out ranges (outputs) overlaps any other.
+bool outputs_overlap(const Range* r, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+
 // ------------------------------------------------------------------ matvec
 
 inline size_t type_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
@@ -182,19 +195,6 @@ moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   return ws && aligned(ws, kAlign) && ws_bytes >= need ? MOE_OK : MOE_ERR_WORKSPACE;
 }
 
-struct Range {
-  const void* p;
-  size_t n;
-};
-
-// Whether one of the first n_out ranges (outputs) overlaps any other.
-bool outputs_overlap(const Range* r, int n_out, int n) {
-  for (int i = 0; i < n_out; ++i)
-    for (int j = i + 1; j < n; ++j)
-      if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
-  return false;
-}
-
 inline size_t weight_bytes(const moe_ffn* F) {
   const size_t n = (size_t)F->d * F->f;
   return is_16bit(F) ? 2 * n : n / 2;
@@ -256,15 +256,16 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   if (!x || !aligned(x, 16) || !y || !aligned(y, type_bytes(M->y_type))) return MOE_ERR_INVALID_ARG;
   const size_t T = M->T, N = M->N, K = M->K;
   const size_t yb = ((T - 1) * (size_t)M->ldy + N) * type_bytes(M->y_type);
-  if (overlap(y, yb, x, ((T - 1) * (size_t)M->ldx + K) * 2) || overlap(y, yb, M->w, N * K / 2) ||
-      overlap(y, yb, M->s, N * (K / M->group) * 2) || overlap(y, yb, M->bias, N * 4))
-    return MOE_ERR_INVALID_ARG;
+  Range r[] = {{y, yb}, {ws, 0}, {x, ((T - 1) * (size_t)M->ldx + K) * 2}, {M->w, N * K / 2},
+               {M->s, N * (K / M->group) * 2}, {M->bias, N * 4}};
+  if (outputs_overlap(r, 1, 6)) return MOE_ERR_INVALID_ARG;
   GemvArgs a = matvec_args(M);
   size_t part, cnt;
   gemv_scratch(a, &part, &cnt);
   const GemvWs w = matvec_ws(part, cnt);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
-  if (overlap(y, yb, ws, w.total)) return MOE_ERR_INVALID_ARG;
+  r[1].n = w.total;  // (it holds partial sums and counters while inputs are still read)
+  if (outputs_overlap(r, 2, 6)) return MOE_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.status = reinterpret_cast<int32_t*>(base);
   a.x = static_cast<const uint16_t*>(x);

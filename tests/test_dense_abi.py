@@ -265,3 +265,21 @@ def test_results_are_allocated_for_the_stream_of_the_call(monkeypatch, stream):
     assert [tuple(g.shape) for g in grads] == [(2, 8), (16, 8), (16, 8), (8, 16)]
     want = 0 if stream is None else stream.cuda_stream
     assert allocations == [want] * 6 and launches == [want] * 3
+
+
+def test_matvec_refuses_a_workspace_over_its_inputs(lib):
+    """A call with K in parts writes partial sums and counters while inputs are still read."""
+    m = matrix(T=32, N=1000, K=10240, ldx=10240)
+    p = [(i + 2) << 36 for i in range(6)]
+    m.w, m.s, m.bias, x, y, ws = p
+    need = lib.moe_matvec_workspace_size(ctypes.byref(m))
+    assert need > 256 + 4 * 8192                         # split
+    call = lambda ws: lib.moe_matvec(ctypes.byref(m), x, y, ws, need, None)  # noqa: E731
+    sizes = {m.w: 1000 * 10240 // 2, m.s: 1000 * 80 * 2, m.bias: 4000, x: 32 * 10240 * 2}
+    for at, size in sizes.items():
+        for off in (0, size // 2 // 256 * 256, (size - 1) // 256 * 256, -256, -(need - 256)):
+            assert call(at + off) == -1, (at, off)
+    m.K, m.ldx = 2560, 2560                              # not split: the status words alone
+    m.T, need = 1, 256
+    assert lib.moe_matvec_workspace_size(ctypes.byref(m)) == need
+    assert call(x) == -1 and call(m.w) == -1
