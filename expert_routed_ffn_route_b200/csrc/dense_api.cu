@@ -39,6 +39,17 @@ bool outputs_overlap(const Range* r, int n_out, int n) {
 
 // ------------------------------------------------------------------ matvec
 
+// Whether a row of a (an bytes, rows as bytes apart) shares a byte with a row of b: both may be
+// columns of one wider array, whose rows interleave without overlapping.
+bool rows_overlap(const void* a, size_t an, size_t as, const void* b, size_t bn, size_t bs, int T) {
+  if (!overlap(a, (T - 1) * as + an, b, (T - 1) * bs + bn)) return false;
+  for (int i = 0; i < T; ++i)
+    for (int j = 0; j < T; ++j)
+      if (overlap(static_cast<const char*>(a) + i * as, an, static_cast<const char*>(b) + j * bs, bn))
+        return true;
+  return false;
+}
+
 inline size_t type_bytes(int t) { return t == MOE_T_FP32 ? 4 : 2; }
 
 moe_status matvec_validate(const moe_matrix* M) {
@@ -255,17 +266,21 @@ moe_status moe_matvec(const moe_matrix* M, const void* x, void* y, void* ws, siz
   if (s != MOE_OK) return s;
   if (!x || !aligned(x, 16) || !y || !aligned(y, type_bytes(M->y_type))) return MOE_ERR_INVALID_ARG;
   const size_t T = M->T, N = M->N, K = M->K;
-  const size_t yb = ((T - 1) * (size_t)M->ldy + N) * type_bytes(M->y_type);
-  Range r[] = {{y, yb}, {ws, 0}, {x, ((T - 1) * (size_t)M->ldx + K) * 2}, {M->w, N * K / 2},
-               {M->s, N * (K / M->group) * 2}, {M->bias, N * 4}};
-  if (outputs_overlap(r, 1, 6)) return MOE_ERR_INVALID_ARG;
+  const size_t ysize = type_bytes(M->y_type), yb = ((T - 1) * (size_t)M->ldy + N) * ysize;
+  const Range y_r{y, yb}, x_r{x, ((T - 1) * (size_t)M->ldx + K) * 2}, w_r{M->w, N * K / 2},
+      s_r{M->s, N * (K / M->group) * 2}, b_r{M->bias, N * 4};
+  const Range out[] = {y_r, w_r, s_r, b_r};
+  if (outputs_overlap(out, 1, 4) ||
+      rows_overlap(y, N * ysize, M->ldy * ysize, x, K * 2, M->ldx * 2, M->T))
+    return MOE_ERR_INVALID_ARG;
   GemvArgs a = matvec_args(M);
   size_t part, cnt;
   gemv_scratch(a, &part, &cnt);
   const GemvWs w = matvec_ws(part, cnt);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
-  r[1].n = w.total;  // (it holds partial sums and counters while inputs are still read)
-  if (outputs_overlap(r, 2, 6)) return MOE_ERR_INVALID_ARG;
+  // (the workspace holds partial sums and counters while inputs are still read)
+  const Range held[] = {{ws, w.total}, y_r, x_r, w_r, s_r, b_r};
+  if (outputs_overlap(held, 1, 6)) return MOE_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.status = reinterpret_cast<int32_t*>(base);
   a.x = static_cast<const uint16_t*>(x);

@@ -311,7 +311,7 @@ MOE_API moe_status moe_nvfp4_quantize_rows(const float* v, int32_t rows, int32_t
  * MOE_T_BF16 or MOE_T_FP16; y_type x_type or MOE_T_FP32. ldx, ldy: elements between rows
  * (ldx >= K and a multiple of 8, ldy >= N). w and x 16-byte aligned, s 2, y 4 for fp32 and
  * else 2, bias (fp32 [N] or NULL) 4. y and the workspace must not overlap each other or an
- * input. */
+ * input (rows of x and y may interleave, as columns of one wider array do). */
 typedef struct {
   int32_t T, N, K, group;
   int32_t x_type, y_type; /* moe_dtype */

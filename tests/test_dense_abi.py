@@ -283,3 +283,26 @@ def test_matvec_refuses_a_workspace_over_its_inputs(lib):
     m.T, need = 1, 256
     assert lib.moe_matvec_workspace_size(ctypes.byref(m)) == need
     assert call(x) == -1 and call(m.w) == -1
+
+
+def test_matvec_takes_columns_of_one_array(lib):
+    """Rows of x and y that interleave without sharing an element (slices of one wider array) are
+    no overlap; one element shared is. (-3: passed on to CUDA, which has no device here.)"""
+    m = matrix(T=8, N=1000, K=2560, ldx=4096, ldy=4096)
+    m.w, m.s, ws, buf = ((i + 2) << 36 for i in range(4))
+    size = lib.moe_matvec_workspace_size(ctypes.byref(m))
+    need = max(size, 256)
+    bad = lambda x, y: lib.moe_matvec(ctypes.byref(m), x, y, ws, need, None) == -1  # noqa: E731
+    assert bad(buf, buf + 2 * 2559) and bad(buf, buf + 2 * 3097)  # x's end; the next row's start
+    assert bad(buf + 2 * 1000, buf + 2 * 3097 + 2 * 1000 - 2 * 4096)
+    assert bad(buf + 2 * 992, buf) and bad(buf, buf)
+    m.y_type = 2                                                # fp32 rows twice as far apart
+    assert bad(buf, buf + 2 * 2560)
+    m.y_type, m.ldy = 0, 4100                                   # rows that drift into x's
+    assert bad(buf, buf + 2 * 2560 + 2 * 530)
+    import torch
+    if not torch.cuda.is_available():
+        m.ldy = 4096
+        for x, y in ((buf, buf + 2 * 2560), (buf, buf + 2 * 3096), (buf + 2 * 1000, buf),
+                     (buf + 2 * 1536, buf)):
+            assert lib.moe_matvec(ctypes.byref(m), x, y, ws, need, None) == -3

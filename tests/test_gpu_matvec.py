@@ -398,3 +398,22 @@ def test_calls_on_a_given_stream_keep_to_their_memory(B):
         junk += [torch.full(shape[1], 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
         torch.cuda.synchronize()
         assert torch.equal(y, want) and B.matvec_device_status(desc, junk[-1].zero_()) == (0, 0)
+
+
+@pytest.mark.parametrize("T", [1, 2, 8, 32])
+def test_rows_and_results_in_one_array(B, T):
+    """x and y as columns of one array: neither touches the other or what lies beside them."""
+    N, K, ld = 500, 1280, 2560
+    desc, x, W, b = make(B, T, N, K, 128, ldx=ld, ldy=ld)
+    buf = torch.full((T, ld), 3.0, dtype=BF, device="cuda")
+    buf[:, 512:512 + K] = x.cuda()
+    for at in (0, 12, 512 + K, ld - N):
+        buf[:, at:at + N] = 7.0
+        B.matvec(desc, buf[:, 512:512 + K], B.alloc_matvec_workspace(desc), out=buf[:, at:at + N])
+        check(buf[:, at:at + N], x, W, b, 128, at)
+        assert torch.equal(buf[:, 512:512 + K].cpu(), x)
+        buf[:, at:at + N] = 3.0
+        assert (buf[:, :512] == 3).all() and (buf[:, 512 + K:] == 3).all()
+    if T > 1:
+        with pytest.raises(B.MoeError):
+            B.matvec(desc, buf[:, 512:512 + K], B.alloc_matvec_workspace(desc), out=buf[:, 13:13 + N])
