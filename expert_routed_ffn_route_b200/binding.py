@@ -504,9 +504,10 @@ class QuantMatrix:
         M.owner = self
         lib = load_library()
         _check(lib.moe_matvec_validate(ctypes.byref(M)), "moe_matvec_validate")
-        # what each call needs, at hand: a call costs the host little more than its launch
+        # what each call needs, at hand: a call costs the host little more than its launch. (No
+        # reference to M itself: the cycle would keep the weights until a garbage collection.)
         M.call = ((T, self.K), (T, self.N), M.ldx, M.ldy, x_dtype, y_dtype, self.device.index,
-                  ctypes.byref(M), lib.moe_matvec)
+                  lib.moe_matvec)
         return M
 
 
@@ -522,7 +523,7 @@ def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     """y = x W^T (+ bias) for the T <= 32 rows of x: [T, K] -> [T, N] (include/moe_b200.h)."""
     if stream is not None:
         return _on(stream, matvec, M, x, ws, out)
-    x_shape, y_shape, ldx, ldy, xt, yt, index, ref, fn = M.call
+    x_shape, y_shape, ldx, ldy, xt, yt, index, fn = M.call
     _check_rows(x, "x", x_shape, xt, index, ldx)
     if out is None:
         # (sizes as numbers: a tuple costs the call half a microsecond more)
@@ -533,7 +534,7 @@ def matvec(M: MoeMatrix, x, ws, out=None, stream=None):
     else:
         _check_rows(out, "out", y_shape, yt, index, ldy)
     _check_ws(ws, index)
-    status = _call(index, fn, ref, x.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+    status = _call(index, fn, M, x.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
     if status:
         _check(status, "moe_matvec")
     return out
@@ -584,7 +585,7 @@ class DeviceFfn:
         F.owner = self
         lib = load_library()
         _check(lib.moe_ffn_validate(ctypes.byref(F)), "moe_ffn_validate")
-        F.call = ((T, self.d), (2, T, self.f), self.dtype, self.device.index, ctypes.byref(F),
+        F.call = ((T, self.d), (2, T, self.f), self.dtype, self.device.index,
                   lib.moe_ffn_forward, lib.moe_ffn_backward)
         return F
 
@@ -620,7 +621,7 @@ def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     ffn_backward needs (include/moe_b200.h)."""
     if stream is not None:
         return _on(stream, ffn_forward, F, x, ws, out, pre)
-    shape, pre_shape, dtype, index, ref, fn, _ = F.call
+    shape, pre_shape, dtype, index, fn, _ = F.call
     _check_rows(x, "x", shape, dtype, index)
     if out is None:
         out = x.new_empty(*shape)
@@ -629,7 +630,7 @@ def ffn_forward(F: MoeFfn, x, ws, out=None, pre=None, stream=None):
     if pre is not None:
         _check_pre(pre, pre_shape, index)
     _check_ws(ws, index)
-    status = _call(index, fn, ref, x.data_ptr(), out.data_ptr(), _ptr(pre), ws.data_ptr(),
+    status = _call(index, fn, F, x.data_ptr(), out.data_ptr(), _ptr(pre), ws.data_ptr(),
                    ws.numel())
     if status:
         _check(status, "moe_ffn_forward")
@@ -642,7 +643,7 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
     not needed is None and not computed. ``ws``: alloc_ffn_workspace(F, backward=True)."""
     if stream is not None:
         return _on(stream, ffn_backward, F, x, dy, pre, ws, need_dx, need_dw)
-    shape, pre_shape, dtype, index, ref, _, fn = F.call
+    shape, pre_shape, dtype, index, _, fn = F.call
     _check_rows(x, "x", shape, dtype, index)
     _check_rows(dy, "dy", shape, dtype, index)
     _check_pre(pre, pre_shape, index)
@@ -651,7 +652,7 @@ def ffn_backward(F: MoeFfn, x, dy, pre, ws, need_dx: bool = True, need_dw: bool 
     dwg = dwu = dwd = None
     if need_dw:
         dwg, dwu, dwd = x.new_empty(F.f, F.d), x.new_empty(F.f, F.d), x.new_empty(F.d, F.f)
-    _check(_call(index, fn, ref, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), _ptr(dx),
+    _check(_call(index, fn, F, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), _ptr(dx),
                  _ptr(dwg), _ptr(dwu), _ptr(dwd), ws.data_ptr(), ws.numel()), "moe_ffn_backward")
     return dx, dwg, dwu, dwd
 

@@ -254,11 +254,11 @@ def test_results_are_allocated_for_the_stream_of_the_call(monkeypatch, stream):
     allocations, launches, accept, torch = calls_on_a_fake_device(monkeypatch)
     bf = torch.bfloat16
     ws = torch.zeros(256, dtype=torch.uint8)
-    M = SimpleNamespace(call=((2, 8), (2, 4), 8, 4, bf, bf, -1, None, accept))
+    M = SimpleNamespace(call=((2, 8), (2, 4), 8, 4, bf, bf, -1, accept))
     x = torch.zeros(2, 8, dtype=bf)
     y = binding.matvec(M, x, ws, stream=stream)
     assert y.shape == (2, 4)
-    F = SimpleNamespace(call=((2, 8), (2, 2, 16), bf, -1, None, accept, accept), d=8, f=16)
+    F = SimpleNamespace(call=((2, 8), (2, 2, 16), bf, -1, accept, accept), d=8, f=16)
     pre = torch.zeros(2, 2, 16)
     y = binding.ffn_forward(F, x, ws, pre=pre, stream=stream)
     grads = binding.ffn_backward(F, x, y, pre, ws, stream=stream)
@@ -306,3 +306,33 @@ def test_matvec_takes_columns_of_one_array(lib):
         for x, y in ((buf, buf + 2 * 2560), (buf, buf + 2 * 3096), (buf + 2 * 1000, buf),
                      (buf + 2 * 1536, buf)):
             assert lib.moe_matvec(ctypes.byref(m), x, y, ws, need, None) == -3
+
+
+@pytest.mark.parametrize("kind", ["matrix", "block"])
+def test_a_descriptor_lets_go_of_the_weights(lib, kind):
+    """Weights are freed with the last descriptor, without the garbage collector (which GPU memory
+    does not wake), and live as long as one."""
+    import gc
+    import weakref
+    torch = pytest.importorskip("torch")
+    if kind == "matrix":
+        owner = binding.QuantMatrix.__new__(binding.QuantMatrix)
+        owner.codes, owner.bias = torch.zeros(4, 16, dtype=torch.int32), None
+        owner.scales = torch.zeros(4, 1, dtype=torch.bfloat16)
+        owner.N, owner.K, owner.group, owner.device = 4, 128, 128, torch.device("cpu")
+    else:
+        owner = binding.DeviceFfn.__new__(binding.DeviceFfn)
+        w = torch.zeros(8, 8, dtype=torch.bfloat16)
+        owner.bank = dict(fmt="bf16", group=128, n_exp=1, w_gate=w, w_up=w, w_down=w)
+        owner.d, owner.f, owner.act, owner.dtype, owner.device = 8, 8, "silu", w.dtype, w.device
+    alive, desc = weakref.ref(owner), owner.descriptor(1)
+    on = gc.isenabled()
+    gc.disable()
+    try:
+        del owner
+        assert alive() is not None
+        del desc
+        assert alive() is None
+    finally:
+        if on:
+            gc.enable()
