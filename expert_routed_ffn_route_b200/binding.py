@@ -65,7 +65,8 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_s
            "moe_nvfp4_pack_scales", "moe_nvfp4_quantize_rows", "moe_device_wait_site",
            "moe_matvec_validate", "moe_matvec_workspace_size", "moe_matvec",
            "moe_matvec_device_status", "moe_ffn_validate", "moe_ffn_workspace_size",
-           "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_device_status"]
+           "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_device_status",
+           "moe_test_inject_dense_hold"]
 
 
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
@@ -114,6 +115,7 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "moe_ffn_forward": (I32, [FP, P, P, P, P, SZ, P]),
         "moe_ffn_backward": (I32, [FP, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_ffn_device_status": (I32, [FP, P, SZ, ctypes.POINTER(I32), ctypes.POINTER(I32), P]),
+        "moe_test_inject_dense_hold": (I32, [I32, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -674,3 +676,10 @@ def ffn_device_status(F: MoeFfn, ws, stream=None):
 def matvec_device_status(M: MoeMatrix, ws, stream=None):
     """(status code, wait site) kept in a matvec workspace since the last read (0, 0: none)."""
     return _device_status(load_library().moe_matvec_device_status, M, ws, stream)
+
+
+def test_inject_dense_hold(hold: bool, budget_cycles: int = 0):
+    """Sets or clears the dense operators' failure injection for this thread's calls (see the
+    header)."""
+    _check(load_library().moe_test_inject_dense_hold(int(bool(hold)), int(budget_cycles)),
+           "moe_test_inject_dense_hold")

@@ -23,6 +23,13 @@ int device_sms();
 // `done` is the kernel's own array of kMaxDevices flags.
 cudaError_t allow_smem(const void* kernel, std::atomic<bool>* done);
 
+// Test control of the calling thread's launches (moe_test_inject_dense_hold). It is a kernel
+// argument: a word in the workspace, as the layer's, cost ordinary calls 1 to 4 %.
+struct TestHold {
+  int hold = 0, budget = 0;
+};
+extern thread_local TestHold g_test_hold;
+
 // Starts the fetch of a tensor map (a kernel's first TMA copy waits for its map otherwise).
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -303,6 +303,13 @@ moe_status moe_matvec_device_status(const moe_matrix* M, void* ws, size_t ws_byt
   return read_status(ws, code, site, reinterpret_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_test_inject_dense_hold(int32_t hold, int32_t budget_cycles) {
+  if (budget_cycles < 0) return MOE_ERR_INVALID_ARG;
+  g_test_hold.hold = hold != 0;
+  g_test_hold.budget = budget_cycles;
+  return MOE_OK;
+}
+
 moe_status moe_ffn_validate(const moe_ffn* F) { return ffn_validate(F); }
 
 size_t moe_ffn_workspace_size(const moe_ffn* F, int32_t backward) {

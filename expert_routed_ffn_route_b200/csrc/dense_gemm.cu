@@ -91,6 +91,7 @@ struct GemmArgs {
   float* partial;     // [unit][rank][BN * 128]
   int32_t* counters;  // [slot][rank][warp], zero between launches
   int keep;           // EPI_GATED: write g and u
+  int hold;           // test control: the issuer gives up at its first wait
   int32_t* status;
 };
 
@@ -407,13 +408,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
       }
       if (!ok) fail(50);
-      // every issued stage lands before the pair may exit (the leader waits for all shares)
+      // every issued stage lands before the pair may exit (the leader waits for all shares; after a
+      // timeout one may lack a share that another producer no longer brought: it uses the bound up,
+      // the rest is only looked at)
+      long long left = kWaitCycles;
       if (rank == 0 && is_a)
         for (int j = 0; j < min(it, C::NS); ++j, ring.next()) {
           // the last use of each stage, oldest first
           const bool wrapped = it > C::NS;
           const int s = wrapped ? ring.s : j;
-          mbar_wait(&full[s], wrapped ? ring.phase ^ 1 : 0);
+          if (!mbar_wait(&full[s], wrapped ? ring.phase ^ 1 : 0, left)) left = 0;
         }
     }
     __syncwarp();
@@ -421,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
       int tile = 0;
-      bool aborted = false;
+      bool aborted = a.hold != 0;
       const uint32_t stage0 = smem_u32(smem);
       for (; !aborted && walk.next(a, &u); ++tile) {
         const GemmProblem& q = a.p[u.p];
@@ -1026,6 +1030,7 @@ cudaError_t run_products(const Product* pr, int n, const FfnArgs& f, cudaStream_
   a.partial = f.partial;
   a.counters = f.counters;
   a.keep = f.pre != nullptr;
+  a.hold = g_test_hold.hold;
   // outputs (and the gate gradient's inputs) by blocks of 32 rows
   const int cols = EPI == EPI_GATED ? bn / 4 : bn / 2;
   const int ch = EPI == EPI_GRAD ? 16 : std::min(cols, EPI == EPI_GATED ? 32 : 64);

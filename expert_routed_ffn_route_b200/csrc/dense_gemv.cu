@@ -75,6 +75,8 @@ struct GemvPlan {
   int wpr;           // log2 of the warps that stage one row
   int depth;         // ring slots a warp
   int early;         // the kernel before writes no weights
+  int drop;          // test control: warp 0 leaves its first copy out
+  long long limit;   // cycles after which a wait gives up
   int smem;
 };
 
@@ -122,7 +124,8 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   p.tiles_r = p.tiles % p.groups;
   p.wpr = 0;
   while ((kWarps >> (p.wpr + 1)) >= a.T) ++p.wpr;
-  p.early = 0;
+  p.early = p.drop = 0;
+  p.limit = kWaitCycles;
   p.smem = p.depth * kRingSlot + xbytes + 2048;
   return p;
 }
@@ -248,10 +251,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   uint8_t* ring = smem + warp * (p.depth * kSlotBytes);
   uint64_t* full = bars + warp * kMaxDepth;
   int ct = tile0, cs = slot0, cstage = 0, cleft = n_my;  // copy cursor
-  auto copy_next = [&]() {
+  auto copy_next = [&](bool drop = false) {
     if (cleft <= 0) return;
     --cleft;
-    if (lane == 0) {
+    if (lane == 0 && !drop) {
       uint8_t* dst = ring + cstage * kSlotBytes;
       const int x = begin * 64 + cs * 128;
       mbar_arrive_expect_tx(&full[cstage], kSlotBytes);
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       fence_barrier_init();
     }
     __syncwarp();
-    for (int i = 0; i < p.depth; ++i) copy_next();
+    for (int i = 0; i < p.depth; ++i) copy_next(p.drop && warp == 0 && i == 0);
   };
 
   // ---- scales: a slot ahead, in registers. A quad's lanes hold row half t4 / 2, unit t4 % 2.
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int j = 0; j < NSC; ++j) sc[j] = __uint_as_float(sn[j] << 16);
       load_scales();
       const uint8_t* sp = ring + stage * kSlotBytes;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, p.limit))) {
         set_timeout(a.status, kSiteGemvSlot);
         ok = false;                                // no more copies; those on the way are waited
         pending = n_my - cleft - it;               // for below
@@ -662,9 +665,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   else run(std::false_type{});
 
   // after a timeout: the copies still on the way land (or their waits give up) before the ring is
-  // written or the CTA ends
+  // written or the CTA ends (one that does not within the bound leaves none to the rest)
+  long long left = kWaitCycles;
   for (; pending > 0; --pending) {
-    mbar_wait(&full[bad_stage], bad_phase);
+    if (!mbar_wait(&full[bad_stage], bad_phase, left)) left = 0;
     if (++bad_stage == p.depth) {
       bad_stage = 0;
       bad_phase ^= 1;
@@ -799,6 +803,8 @@ cudaError_t launch_fmt(const GemvArgs& a, const GemvPlan& p, cudaStream_t st) {
 
 }  // namespace
 
+thread_local TestHold g_test_hold;
+
 int device_sms() {
   static std::atomic<int> sms[kMaxDevices];
   int dev = 0;
@@ -833,6 +839,10 @@ cudaError_t launch_gemv_rows(const GemvArgs& a, cudaStream_t st, bool early) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   GemvPlan p = make_gemv_plan(a, sms);
   p.early = early;
+  if (g_test_hold.hold) {
+    p.drop = 1;
+    if (g_test_hold.budget > 0) p.limit = g_test_hold.budget;
+  }
   if (p.smem > kSmemMax || p.parts > sms) return cudaErrorInvalidValue;
   return a.f16 ? launch_fmt<true>(a, p, st) : launch_fmt<false>(a, p, st);
 }

@@ -391,6 +391,16 @@ MOE_API moe_status moe_ffn_backward(const moe_ffn* F, const void* x, const void*
 MOE_API moe_status moe_ffn_device_status(const moe_ffn* F, void* ws, size_t ws_bytes,
                                          int32_t* code, int32_t* site, moe_stream_t stream);
 
+/* Failure injection for tests of the dense operators' error path. While it is set (hold != 0),
+ * one wait in every dense kernel that the calling thread launches runs out: a streaming CTA's
+ * first warp leaves its first copy out and gives up on it after budget_cycles SM clock cycles
+ * (0 = the normal bound of about two seconds) and, with the copies that are on their way, once
+ * more after the normal bound (site 60); the issuer of a tensor-core pair gives up at once (site
+ * 51), whereupon the pair's other waits run out after the normal bound. The kernels record
+ * MOE_ERR_TIMEOUT, wait for their copies and return; results of such a call are undefined.
+ * hold == 0 ends it; the workspace is zeroed before its next use, as after any timeout. */
+MOE_API moe_status moe_test_inject_dense_hold(int32_t hold, int32_t budget_cycles);
+
 #ifdef __cplusplus
 }
 #endif

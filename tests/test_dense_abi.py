@@ -336,3 +336,9 @@ def test_a_descriptor_lets_go_of_the_weights(lib, kind):
     finally:
         if on:
             gc.enable()
+
+
+def test_failure_injection_is_checked(lib):
+    assert lib.moe_test_inject_dense_hold(1, -1) == -1
+    assert lib.moe_test_inject_dense_hold(1, 1000) == 0
+    assert lib.moe_test_inject_dense_hold(0, 0) == 0
