@@ -342,3 +342,22 @@ def test_failure_injection_is_checked(lib):
     assert lib.moe_test_inject_dense_hold(1, -1) == -1
     assert lib.moe_test_inject_dense_hold(1, 1000) == 0
     assert lib.moe_test_inject_dense_hold(0, 0) == 0
+
+
+def test_the_plain_dequantisation_is_the_oracles():
+    """The weights that the GPU tests compare with, against the oracle's reading of the same words
+    (every nibble value, the sign bit of a word included)."""
+    import numpy as np
+    torch = pytest.importorskip("torch")
+    from dense_helpers import dequantise, pack
+    from oracle import moe_oracle as O
+    gen = torch.Generator().manual_seed(2)
+    q = torch.randint(-8, 8, (24, 512), generator=gen)
+    words = pack(q)
+    assert (words < 0).any() and (words > 0).any() and len(q.unique()) == 16
+    for group in (32, 64, 128):
+        s = torch.randn(24, 512 // group, generator=gen).to(torch.bfloat16)
+        W = O.dequantize(words.numpy().view(np.uint32), s.view(torch.int16).numpy().view(np.uint16),
+                         "int4", group, 512)
+        assert np.array_equal(W, dequantise(words, s, group).numpy())
+        assert np.array_equal(W, (q.double() * s.double().repeat_interleave(group, 1)).numpy())

@@ -417,3 +417,34 @@ def test_rows_and_results_in_one_array(B, T):
     if T > 1:
         with pytest.raises(B.MoeError):
             B.matvec(desc, buf[:, 512:512 + K], B.alloc_matvec_workspace(desc), out=buf[:, 13:13 + N])
+
+
+def test_an_experts_matrices_as_the_oracle_reads_them(B):
+    """The three matrices of one expert of an int4 bank, as products against the oracle's
+    dequantised weights, and as a dense block against the oracle's expert."""
+    import numpy as np
+    from dense_helpers import assert_norm_close, ffn_ref
+    from expert_routed_ffn_route_b200 import synth
+    from oracle import moe_oracle as O
+    cfg = synth.LayerConfig("mv", T=3, d=256, E=4, k=2, f=384, fmt="int4", seed=6)
+    L = synth.make_layer(cfg)
+    dl, arrays, e = B.DeviceLayer(L), L.routed.arrays(), 1
+    bank, W = dl.banks["routed"], []
+    gen = torch.Generator().manual_seed(3)
+    for m, N, K in (("gate", cfg.f, cfg.d), ("up", cfg.f, cfg.d), ("down", cfg.d, cfg.f)):
+        W.append(O.dequantize(arrays["w_" + m][e], arrays["s_" + m][e], "int4", 128, K))
+        assert W[-1].shape == (N, K)
+        x = torch.randn(3, K, generator=gen).to(BF)
+        desc = B.QuantMatrix(bank["w_" + m][e], bank["s_" + m][e], K).descriptor(3, y_dtype=F32)
+        check(B.matvec(desc, x.cuda(), B.alloc_matvec_workspace(desc)), x, torch.from_numpy(W[-1]),
+              None, 128, m)
+    block = B.DeviceFfn({k: v if isinstance(v, (str, int)) else v[e] for k, v in bank.items()
+                         if k != "n_exp"}, cfg.d, cfg.f)
+    x = torch.randn(3, cfg.d, generator=gen).to(BF)
+    desc = block.descriptor(3)
+    y = B.ffn_forward(desc, x.cuda(), B.alloc_ffn_workspace(desc))
+    want = torch.from_numpy(O.expert_ffn(x.double().numpy(), *W))
+    bound = ffn_ref(x, *(torch.from_numpy(w) for w in W), "silu", BF)["y"][1]
+    assert np.isfinite(want.numpy()).all()
+    assert_close(y, want, bound, BF, "block")
+    assert_norm_close(y, want, BF, "block")
