@@ -306,7 +306,10 @@ MOE_API moe_status moe_nvfp4_quantize_rows(const float* v, int32_t rows, int32_t
  * their scale, and the result is rounded once to y_type. Large matrices with groups of 128
  * and up to 8 rows sum (q + 8) x and take 8 sum(x) off (both in fp32, so their rounding is
  * relative to (|q| + 8) |x|), unless the rows hold infinities, NaN, or bf16 magnitudes
- * outside [2^-90, 2^26).
+ * outside [2^-90, 2^26). NOT row-invariant, unlike the layer's AUTO path: results repeat bit for
+ * bit for the same T and rows, but a row's bits depend on T (the split of K, and that form), and
+ * where that form may be taken on whether any row of the call holds such a value. A chain that must
+ * reproduce single-row results bit for bit calls with T = 1.
  * 1 <= T <= 32, N >= 1, group 32, 64 or 128, K % group == 0, 1 <= K <= 32768, N <= 2^24. x_type
  * MOE_T_BF16 or MOE_T_FP16; y_type x_type or MOE_T_FP32. ldx, ldy: elements between rows
  * (ldx >= K and a multiple of 8, ldy >= N). w and x 16-byte aligned, s 2, y 4 for fp32 and
@@ -354,8 +357,14 @@ MOE_API moe_status moe_matvec_device_status(const moe_matrix* M, void* ws, size_
  *                           to 32 rows (MOE_ERR_UNSUPPORTED beyond).
  * Products are summed in fp32; h, dg and du are rounded to the 16-bit type (the next product's
  * operand: an h, dg or du beyond fp16's 65504 becomes infinite), g and u are kept in fp32, dh is
- * never stored. Every pointer is 16-byte aligned (int4 scales: 2) and rows are dense. Outputs
- * must not overlap each other or an input. */
+ * never stored. Every pointer is 16-byte aligned (int4 scales: 2) and rows are dense. Outputs and
+ * the workspace must not overlap each other or an input.
+ * NOT row-invariant: as for moe_matvec; beyond 256 rows a row's bits depend on its place too (its
+ * tile may be one that is summed in parts); up to 4 streamed rows carry h as two 16-bit rows (the
+ * rounded value and the rest), so that y is rounded once there and twice from 5 rows on. A block in
+ * silu is also a layer of one expert (E = k = 1, no shared expert; d and f multiples of 128, up to
+ * 8192): that route is row-invariant up to 32 rows and takes int8 and more than 32 int4 rows, and is
+ * slower (2560 x 1024, int4, 1 / 16 / 32 rows 16.8 / 50 / 86 us against 7.9 / 12.9 / 16.2 here). */
 typedef struct {
   int32_t T, d, f;
   int32_t act; /* moe_act */

@@ -588,3 +588,43 @@ def test_a_step_on_a_given_stream_keeps_to_its_memory(B):
     if torch.cuda.device_count() > 1:
         with pytest.raises(ValueError):
             B.ffn_forward(desc, x, B.alloc_ffn_workspace(desc), stream=torch.cuda.Stream(device=1))
+
+
+@pytest.mark.parametrize("fmt", [None, "int4"])
+@pytest.mark.parametrize("T", [4, 20, 200])
+def test_a_row_among_others(B, T, fmt):
+    """At the same number of rows (up to 256, one row tile) a row's result, and its row of dx, have
+    the same bits wherever it stands and whatever the others hold."""
+    if fmt and T > 32:
+        return
+    block, _ = make(B, 256, 384, fmt=fmt)
+    desc = block.descriptor(T)
+    x, dy = rows(T, 256, BF, 31), rows(T, 256, BF, 32)
+    x2, dy2 = rows(T, 256, BF, 33), rows(T, 256, BF, 34)
+    x2[0], dy2[0] = x[T - 1], dy[T - 1]
+    ws = B.alloc_ffn_workspace(desc)
+    assert torch.equal(B.ffn_forward(desc, x, ws)[T - 1], B.ffn_forward(desc, x2, ws)[0])
+    if not fmt:
+        ws, pre, dx = B.alloc_ffn_workspace(desc, backward=True), B.ffn_pre(desc), []
+        for a, b in ((x, dy), (x2, dy2)):
+            B.ffn_forward(desc, a, ws, pre=pre)
+            dx.append(B.ffn_backward(desc, a, b, pre, ws, need_dw=False)[0])
+        assert torch.equal(dx[0][T - 1], dx[1][0])
+
+
+@pytest.mark.parametrize("fmt,T", [("int4", 1), ("int4", 5), ("int4", 32), ("bf16", 3), ("bf16", 40)])
+def test_a_block_is_a_layer_of_one_expert(B, fmt, T):
+    """The two routes to a silu block agree: the routed layer with one expert and the block."""
+    from types import SimpleNamespace
+    d, f = 256, 384
+    block, W = make(B, d, f, fmt="int4" if fmt == "int4" else None)
+    bank = {k: v if isinstance(v, (str, int)) else v[None] for k, v in block.bank.items()}
+    gate = torch.zeros(1, d, dtype=BF, device="cuda")
+    dl = B.DeviceLayer.from_tensors(SimpleNamespace(d=d, f=f, E=1, k=1), gate, None, bank, None)
+    ld, bd = dl.descriptor(T), block.descriptor(T)
+    x = rows(T, d, BF, 41)
+    ref, bound = ffn_ref(x, *W, "silu", BF)["y"]
+    for y in (B.layer_forward(ld, x, B.alloc_workspace(ld)),
+              B.ffn_forward(bd, x, B.alloc_ffn_workspace(bd))):
+        assert_close(y, ref, bound, BF, fmt)
+        assert_norm_close(y, ref, BF, fmt)

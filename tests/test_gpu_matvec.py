@@ -448,3 +448,22 @@ def test_an_experts_matrices_as_the_oracle_reads_them(B):
     assert np.isfinite(want.numpy()).all()
     assert_close(y, want, bound, BF, "block")
     assert_norm_close(y, want, BF, "block")
+
+
+@pytest.mark.parametrize("x_dtype", [BF, HF])
+def test_large_matrix_a_row_among_ordinary_rows(B, big, x_dtype):
+    """In the shifted form too, at the same number of rows, a row has the same bits whatever
+    ordinary values the others hold; beside a NaN (the other form) it is within the bound."""
+    m, W, scales = big
+    gen = torch.Generator().manual_seed(21)
+    x = torch.randn(8, BIG[1], generator=gen).to(x_dtype)
+    desc = m.descriptor(8, x_dtype=x_dtype, y_dtype=F32)
+    ws = B.alloc_matvec_workspace(desc)
+    y = B.matvec(desc, x.cuda(), ws)
+    other = torch.randn(8, BIG[1], generator=gen).to(x_dtype)
+    other[2] = x[6]
+    assert torch.equal(B.matvec(desc, other.cuda(), ws)[2], y[6])
+    other[5, 17] = float("nan")
+    z = B.matvec(desc, other.cuda(), ws)
+    assert torch.isnan(z[5]).all()
+    check_shifted(z[2:3], x[6:7], W, scales)
