@@ -30,6 +30,16 @@ struct TestHold {
 };
 extern thread_local TestHold g_test_hold;
 
+// mbar_wait with a bound of its own.
+__device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > limit) return false;
+  }
+  return true;
+}
+
 // Starts the fetch of a tensor map (a kernel's first TMA copy waits for its map otherwise).
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

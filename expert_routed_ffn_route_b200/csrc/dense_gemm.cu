@@ -417,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           // the last use of each stage, oldest first
           const bool wrapped = it > C::NS;
           const int s = wrapped ? ring.s : j;
-          if (!mbar_wait(&full[s], wrapped ? ring.phase ^ 1 : 0, left)) left = 0;
+          if (!mbar_wait_within(&full[s], wrapped ? ring.phase ^ 1 : 0, left)) left = 0;
         }
     }
     __syncwarp();

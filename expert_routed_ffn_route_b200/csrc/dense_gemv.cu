@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int j = 0; j < NSC; ++j) sc[j] = __uint_as_float(sn[j] << 16);
       load_scales();
       const uint8_t* sp = ring + stage * kSlotBytes;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, p.limit))) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_within(&full[stage], phase, p.limit))) {
         set_timeout(a.status, kSiteGemvSlot);
         ok = false;                                // no more copies; those on the way are waited
         pending = n_my - cleft - it;               // for below
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   // written or the CTA ends (one that does not within the bound leaves none to the rest)
   long long left = kWaitCycles;
   for (; pending > 0; --pending) {
-    if (!mbar_wait(&full[bad_stage], bad_phase, left)) left = 0;
+    if (!mbar_wait_within(&full[bad_stage], bad_phase, left)) left = 0;
     if (++bad_stage == p.depth) {
       bad_stage = 0;
       bad_phase ^= 1;
