@@ -143,10 +143,16 @@ moe_status ffn_validate(const moe_ffn* F) {
   return MOE_OK;
 }
 
-// Up to 32 rows the weights are streamed through the GEMV kernels (32 rows bf16, streamed / on the
-// tensor cores: 2560 x 1024 16.0 / 18.5 us, 2560 x 10240 46 / 49, 512 x 1024 12.6 / 12.1; one shape
-// measured is better off there from 16 rows: 4096 x 4096 37.5 / 34.3, 4 rows 30.9 / 43.6); a call
-// that keeps g and u for a backward pass takes the tensor-core kernels at any T (they write them).
+// Up to 32 rows the weights are streamed through the GEMV kernels. bf16, us streamed / on the tensor
+// cores (neither keeping g and u):
+//             512 x 1024   1024 x 4096  2560 x 1024  4096 x 2048  4096 x 4096  2560 x 10240
+//   8 rows    6.2 / 11.7   12.3 / 21.4  9.5 / 19.5   17.0 / 31.6  33.3 / 45.5  39.6 / 59.5
+//   16        8.3 / 11.7   14.3 / 19.6  12.7 / 19.5  19.2 / 27.6  37.3 / 33.2  38.9 / 61.9
+//   32        12.4 / 11.7  17.7 / 19.4  15.9 / 18.1  25.5 / 25.7  39.9 / 33.5  46.0 / 48.0
+// So two of the six are better off on the tensor cores below the limit (512 x 1024 at 32 rows, by 6 %;
+// 4096 x 4096 from 16 rows, by 8 to 19 %): the limit is one number for all widths, and a rule with the
+// widths in it is not made. A call that keeps g and u for a backward pass takes the tensor-core
+// kernels at any T (they write them).
 inline bool streams(const moe_ffn* F, const void* pre) {
   return !is_16bit(F) || (F->T <= kGemvMaxRows && !pre);
 }

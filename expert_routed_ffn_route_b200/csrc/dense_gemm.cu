@@ -834,12 +834,14 @@ bool block_map(CUtensorMap* m, const void* base, int rows, int cols, int ch, int
 // The schedule of a launch. Tile width and K splits by estimated cycles, from measured launches: an
 // SM takes in about 46 bytes a cycle (a step of 64 K values brings it (128 + BN / 2) * 128, more
 // than the MMA's 2 BN cycles allow for at every width), and 16 of those that come from DRAM (an
-// operand is counted once for all tiles that share it; forward launches alone: counted for the
-// gradients too, those of 64 rows of 2560 x 10240 take 94 us instead of 91). A tile takes 1500 more
+// operand is counted once for all tiles that share it; in forward launches alone, which is a fit
+// and no model: counted for the gradients too, those of 64 rows of 2560 x 10240 take 94 us instead
+// of 91). A tile takes 1500 more
 // to start and drain, a split one 6000 + 20 BN for the fences and the count, 8 BN to write and
 // 5.5 BN a part to read. With and without the terms 20 BN and DRAM: forward, 64 rows of 2560 x 10240
 // 51.7 / 58.3 us, 301 rows of 4096 x 2048 30.7 / 35.2; gradients, 301 rows of 4096 x 2048 50.4 / 57.0,
-// but 64 rows of 4096 x 2048 44.8 / 42.1 and 200 of 2560 x 10240 100 / 96.
+// but slower: forward, 40 rows of 1024 x 4096 21.9 / 20.3; gradients, 64 rows of 4096 x 2048 44.8 / 42.1
+// and 200 of 2560 x 10240 100 / 96.
 struct GemmPlan {
   Phase ph[kMaxPhases];
   int n_phases, bn, units, slots, pairs;

@@ -98,9 +98,10 @@ GemvPlan make_gemv_plan(const GemvArgs& a, int sms) {
   // K parts: at least so many that a part's rows fit; more where that is estimated shorter (cycles
   // of a CTA, from measured calls): its rows come in at 20 bytes a cycle while every SM fetches
   // the same ones, its slots go through 16 warps, and with parts the sums go through the
-  // workspace. 16 rows on 2560 x 10240, groups of 32: 17.0 us in two parts, 13.7 in seven; 32 rows
-  // on 10240 x 2560: 15.5 in one, 15.1 in two, 17.1 in three. (The SM count is the B200's here: the
-  // workspace's size follows from it.)
+  // workspace. Measured with the number of parts forced: 16 rows on 2560 x 10240, groups of 32: 16.5 us
+  // in two parts, 13.9 in four and in seven, 13.2 in eight (chosen); 32 rows on 10240 x 2560: 14.9 in one,
+  // 14.5 in two (chosen), 16.6 in three; 7 rows on 5003 x 4096: 9.9 in one or two, 9.6 in four (chosen).
+  // (The SM count is the B200's here: the workspace's size follows from it.)
   const int fewest = (p.units + fit - 1) / fit;
   double best = -1;
   for (int parts = fewest; parts <= std::max(fewest, 8); ++parts) {
