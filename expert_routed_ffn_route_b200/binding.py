@@ -241,11 +241,23 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
+def _used_here(stream, *results):
+    """Marks results allocated for a given stream as used by the caller's current stream too: dropped
+    while work queued here still reads them, they are not handed out again before it has run."""
+    import torch
+    if stream is None:
+        return
+    for t in results:
+        if t is not None and t.is_cuda:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def route(L: MoeLayer, x, ws, stream=None):
     import torch
     with _on_stream(stream):
         idx = torch.empty((L.T, L.k), dtype=torch.int32, device=x.device)
         w = torch.empty((L.T, L.k), dtype=torch.float32, device=x.device)
+    _used_here(stream, idx, w)
     _check(load_library().moe_route(ctypes.byref(L), x.data_ptr(), idx.data_ptr(), w.data_ptr(),
                                     ws.data_ptr(), ws.numel(), _stream(stream)), "moe_route")
     return idx, w
@@ -258,6 +270,7 @@ def permute(L: MoeLayer, topk_idx, ws, stream=None):
         offsets = torch.empty(L.E + 1, dtype=torch.int32, device=dev)
         perm = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
         inv = torch.empty(L.T * L.k, dtype=torch.int32, device=dev)
+    _used_here(stream, offsets, perm, inv)
     _check(load_library().moe_permute(ctypes.byref(L), topk_idx.data_ptr(), offsets.data_ptr(),
                                       perm.data_ptr(), inv.data_ptr(), ws.data_ptr(), ws.numel(),
                                       _stream(stream)), "moe_permute")
@@ -270,6 +283,7 @@ def grouped_ffn(L: MoeLayer, x, offsets, perm, ws, has_shared=True, stream=None)
     with _on_stream(stream):
         y_assign = torch.empty((L.T * L.k, L.d), dtype=torch.float32, device=dev)
         y_shared = torch.empty((L.T, L.d), dtype=torch.float32, device=dev) if has_shared else None
+    _used_here(stream, y_assign, y_shared)
     _check(load_library().moe_grouped_ffn(ctypes.byref(L), x.data_ptr(), offsets.data_ptr(),
                                           perm.data_ptr(), y_assign.data_ptr(), _ptr(y_shared),
                                           ws.data_ptr(), ws.numel(), _stream(stream)),
@@ -282,6 +296,7 @@ def combine(L: MoeLayer, y_assign, y_shared, inv, topk_w, out=None, stream=None)
     if out is None:
         with _on_stream(stream):
             out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=y_assign.device)
+        _used_here(stream, out)
     _check(load_library().moe_combine(ctypes.byref(L), y_assign.data_ptr(), _ptr(y_shared),
                                       inv.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
                                       _stream(stream)), "moe_combine")
@@ -295,6 +310,7 @@ def layer_forward(L: MoeLayer, x, ws, out=None, topk_idx=None, topk_w=None, offs
     if out is None:
         with _on_stream(stream):
             out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
+        _used_here(stream, out)
     lib = load_library()
     if marks is None:
         st = lib.moe_layer_forward(ctypes.byref(L), x.data_ptr(), out.data_ptr(), _ptr(topk_idx),
@@ -317,6 +333,7 @@ def nvfp4_pack_scales(src, n_mats: int, rows: int, K: int, stream=None):
     with _on_stream(stream):
         src = src.contiguous()
         dst = torch.empty_like(src)
+    _used_here(stream, dst)
     _check(load_library().moe_nvfp4_pack_scales(src.data_ptr(), dst.data_ptr(), n_mats, rows, K,
                                                 _stream(stream)), "moe_nvfp4_pack_scales")
     return dst
@@ -332,6 +349,7 @@ def nvfp4_quantize_rows(v, stream=None):
         codes = torch.empty((R, K // 2), dtype=torch.uint8, device=v.device)
         scales = torch.empty((R, K // 16), dtype=torch.uint8, device=v.device)
         g = torch.empty(R, dtype=torch.float32, device=v.device)
+    _used_here(stream, codes, scales, g)
     _check(load_library().moe_nvfp4_quantize_rows(v.data_ptr(), R, K, codes.data_ptr(),
                                                   scales.data_ptr(), g.data_ptr(),
                                                   _stream(stream)), "moe_nvfp4_quantize_rows")
@@ -366,6 +384,7 @@ def layer_forward_static(L: MoeLayer, x, out=None, stream=None):
     if out is None:
         with _on_stream(stream):
             out = torch.empty((L.T, L.d), dtype=torch.bfloat16, device=x.device)
+        _used_here(stream, out)
     _check(load_library().moe_layer_forward_static(ctypes.byref(L), x.data_ptr(),
                                                    out.data_ptr(), _stream(stream)),
            "moe_layer_forward_static")
@@ -392,8 +411,8 @@ def test_inject_hold(L: MoeLayer, ws, hold: bool, budget_cycles: int = 0, stream
 # Unlike the layer's calls above, these check their tensors (type, shape, layout, device)
 # before handing over pointers, and raise ValueError. The work runs on the tensors' device,
 # on its current stream unless one is given. A given stream is the current one during the call:
-# its work comes after what that stream holds, results belong to it, and a caller who goes on on
-# another stream orders the two as with torch.cuda.stream.
+# its work comes after what that stream holds, and a caller who goes on on another stream orders
+# the two, as with torch.cuda.stream; the memory of what the call uses and returns is safe to drop.
 
 
 def _dtype_code(t) -> int:
@@ -441,15 +460,15 @@ def _call(index, fn, *args):
         return fn(*args, raw_stream(index))
 
 
-def _on(stream, fn, *args, **kwargs):
-    """fn(*args, **kwargs) with the given `stream` current, so that its results are allocated for
-    that stream (a block of another stream's pool may still be in use by what is queued there).
-    What the call reads and writes is marked as used by the stream: freed early, it is not handed
-    out again before the stream is done with it."""
+def _on(stream, fn, *args):
+    """fn(*args) with the given `stream` current, so that its results are allocated for that stream
+    (a block of another stream's pool may still be in use by what is queued there). What the call
+    reads and writes is marked as used by the stream, and its results as used by the caller's
+    current one: freed early, they are not handed out again before both are done with them."""
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    for a in (*args, *kwargs.values()):
+    for a in args:
         owner = getattr(a, "owner", None)  # a descriptor: its weights
         held = (a,) if owner is None else (*vars(owner).values(), *getattr(owner, "bank", {}).values())
         for t in held:
@@ -459,7 +478,10 @@ def _on(stream, fn, *args, **kwargs):
                                      f"call on {t.device}")
                 t.record_stream(stream)
     with torch.cuda.stream(stream):
-        return fn(*args, **kwargs)
+        result = fn(*args)
+    _used_here(stream, *(t for t in (result if isinstance(result, tuple) else (result,))
+                         if isinstance(t, torch.Tensor)))
+    return result
 
 
 def _alloc_zeroed(nbytes: int, device):

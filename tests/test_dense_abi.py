@@ -361,3 +361,22 @@ def test_the_plain_dequantisation_is_the_oracles():
                          "int4", group, 512)
         assert np.array_equal(W, dequantise(words, s, group).numpy())
         assert np.array_equal(W, (q.double() * s.double().repeat_interleave(group, 1)).numpy())
+
+
+def test_results_are_marked_as_used_by_the_callers_stream(monkeypatch):
+    """A result belongs to the given stream, but the caller reads it on another: dropped there, it
+    waits for both."""
+    from types import SimpleNamespace
+    allocations, launches, accept, torch = calls_on_a_fake_device(monkeypatch)
+    marked = []
+    monkeypatch.setattr(binding, "_used_here", lambda s, *ts: marked.append(
+        (binding._CURRENT[1](-1), s, [tuple(t.shape) for t in ts])))
+    bf, s = torch.bfloat16, FakeStream()
+    ws, x = torch.zeros(256, dtype=torch.uint8), torch.zeros(2, 8, dtype=bf)
+    M = SimpleNamespace(call=((2, 8), (2, 4), 8, 4, bf, bf, -1, accept))
+    F = SimpleNamespace(call=((2, 8), (2, 2, 16), bf, -1, accept, accept), d=8, f=16)
+    pre = torch.zeros(2, 2, 16)
+    binding.matvec(M, x, ws, stream=s)
+    y = binding.ffn_forward(F, x, ws, pre=pre, stream=s)
+    binding.ffn_backward(F, x, y, pre, ws, need_dw=False, stream=s)
+    assert marked == [(0, s, [(2, 4)]), (0, s, [(2, 8)]), (0, s, [(2, 8)])]

@@ -467,3 +467,36 @@ def test_large_matrix_a_row_among_ordinary_rows(B, big, x_dtype):
     z = B.matvec(desc, other.cuda(), ws)
     assert torch.isnan(z[5]).all()
     check_shifted(z[2:3], x[6:7], W, scales)
+
+
+def test_a_result_of_another_stream_dropped_while_it_is_read(B):
+    """A result that work queued here still reads is not overwritten by the next call on the stream
+    that made it; eager, and with the call on a captured side stream."""
+    T, N, K = 32, 8192, 2560
+    desc, x, W, b = make(B, T, N, K, 128)
+    ws, xd = B.alloc_matvec_workspace(desc), x.cuda()
+    want = B.matvec(desc, xd, ws)
+    side, zero = torch.cuda.Stream(), torch.zeros_like(xd)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y = B.matvec(desc, xd, ws, stream=side)
+        side.synchronize()
+        torch.cuda._sleep(20_000_000)
+        copy = y.clone()
+        del y
+        junk = [B.matvec(desc, zero, ws, stream=side) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want) and all((j == 0).all() for j in junk)
+    g, here = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=here):
+        side.wait_stream(here)
+        t = xd + 0
+        y = B.matvec(desc, t, ws, stream=side)
+        del t
+        here.wait_stream(side)
+        z = y + 0
+        y2 = B.matvec(desc, xd, ws, stream=here)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, want) and torch.equal(y2, want)
