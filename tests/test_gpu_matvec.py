@@ -500,3 +500,55 @@ def test_a_result_of_another_stream_dropped_while_it_is_read(B):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(z, want) and torch.equal(y2, want)
+
+
+def test_many_outputs_captured_and_replayed(B):
+    """The call that clears its own counters first, in a graph, twice in a row and over a workspace
+    that another call has filled in between."""
+    T, N, K = 32, 131120, 4096
+    gen = torch.Generator().manual_seed(8)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=gen).to(torch.int32).cuda()
+    scales = (torch.rand(N, K // 128, generator=gen) * 2.0 ** -8 + 2.0 ** -9).to(BF).cuda()
+    m = B.QuantMatrix(codes, scales, K)
+    desc, few = m.descriptor(T), m.descriptor(9)
+    ws = torch.zeros(max(B.matvec_workspace_size(d) for d in (desc, few)), dtype=torch.uint8,
+                     device="cuda")
+    x = torch.randn(T, K, generator=gen).to(BF).cuda()
+    want, want9 = B.matvec(desc, x, ws), B.matvec(few, x[:9], ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = [B.matvec(desc, x, ws), B.matvec(desc, x, ws), B.matvec(few, x[:9], ws),
+               B.matvec(desc, x, ws)]
+    for _ in range(5):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want9 if len(y) == 9 else want) for y in out)
+    assert B.matvec_device_status(desc, ws) == (0, 0)
+
+
+def test_two_host_threads_at_once(B):
+    """Calls from two threads, each with its stream and workspace."""
+    import threading
+    jobs, errors = [], []
+    for seed in (1, 2):
+        desc, x, W, b = make(B, 16, 2560, 10240, 32, seed=seed)
+        jobs.append((desc, x.cuda(), B.alloc_matvec_workspace(desc), torch.cuda.Stream()))
+    want = [B.matvec(desc, x, ws) for desc, x, ws, _ in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            desc, x, ws, s = jobs[i]
+            with torch.cuda.stream(s):
+                for _ in range(200):
+                    y = B.matvec(desc, x, ws)
+                s.synchronize()
+                assert torch.equal(y, want[i])
+        except BaseException as e:  # noqa: BLE001 (reported by the main thread)
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
